@@ -794,3 +794,16 @@ def update_bias(bias: torch.Tensor, counts: torch.Tensor, T: int, K: int, gamma:
     _check(lib.dsmoe_update_bias(_p(bias), _p(counts), bias.numel(), T, K, float(gamma), _stream()),
            "dsmoe_update_bias")
     return bias
+
+
+# The dense feed-forward operators build on the names above.
+from .dense import (ACTIVATIONS, EXPORTED_DENSE, dense_ffn_backward, dense_ffn_forward,  # noqa: E402
+                    gated_linear, gated_linear_backward, gated_linear_backward_workspace_bytes,
+                    gated_linear_workspace_bytes, layer_norm, layer_norm_backward,
+                    layer_norm_backward_workspace_bytes, linear, linear_backward, linear_backward_workspace_bytes,
+                    linear_workspace_bytes)
+
+__all__ += ["ACTIVATIONS", "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes", "linear",
+            "linear_backward", "linear_workspace_bytes", "linear_backward_workspace_bytes", "gated_linear",
+            "gated_linear_backward", "gated_linear_workspace_bytes", "gated_linear_backward_workspace_bytes",
+            "dense_ffn_forward", "dense_ffn_backward"]

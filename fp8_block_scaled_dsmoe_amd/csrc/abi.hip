@@ -4,10 +4,10 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
-#include <cstring>
 #include <mutex>
 
 #include "dsmoe.h"
+#include "host.h"
 #include "kernels.h"
 
 // Scratch of dsmoe_moe_forward_noalloc: one array per GPU, part of the
@@ -20,14 +20,14 @@ static __device__ __align__(256) uint8_t scratch[DSMOE_NOALLOC_SCRATCH_BYTES];
 
 namespace {
 
-constexpr int64_t kI32Max = 2147483647LL;
 constexpr int64_t kMaxK = 32768;   // contraction length limit of the FP8 GEMM (256 chunks)
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-dsmoe_status launch_status(hipError_t e) { return e == hipSuccess ? DSMOE_OK : DSMOE_ERR_LAUNCH; }
+using dsmoe::aligned;
+using dsmoe::check_device;
+using dsmoe::kI32Max;
+using dsmoe::launch_status;
+using dsmoe::round_up;
+using dsmoe::valid_dtype;
 
 std::mutex g_scratch_mu;
 std::atomic<void*> g_scratch_ptr[64];
@@ -46,26 +46,6 @@ void* scratch_for_current_device() {
   }
   return p;
 }
-
-// Device check, cached per device ordinal (idempotent).
-std::atomic<int> g_dev_ok[64];
-
-dsmoe_status check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return DSMOE_ERR_DEVICE;
-  if (dev < 64) {
-    const int v = g_dev_ok[dev].load(std::memory_order_relaxed);
-    if (v == 1) return DSMOE_OK;
-    if (v == 2) return DSMOE_ERR_DEVICE;
-  }
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return DSMOE_ERR_DEVICE;
-  const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-  if (dev < 64) g_dev_ok[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
-  return ok ? DSMOE_OK : DSMOE_ERR_DEVICE;
-}
-
-bool valid_dtype(int t) { return t == DSMOE_BF16 || t == DSMOE_F32; }
 
 dsmoe_status check_routing_shape(int64_t T, int32_t E, int32_t G, int32_t Mg, int32_t K) {
   if (T < 0) return DSMOE_ERR_SHAPE;

@@ -1,0 +1,334 @@
+// The extern "C" boundary of the dense feed-forward operators
+// (dsmoe_dense.h): host-side validation, workspace layout and the order of
+// the launches.  Nothing here allocates device memory.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "dense.h"
+#include "dsmoe_dense.h"
+#include "host.h"
+
+namespace {
+
+using dsmoe::aligned;
+using dsmoe::check_device;
+using dsmoe::DenseEpi;
+using dsmoe::DenseGemm;
+using dsmoe::kI32Max;
+using dsmoe::launch_status;
+using dsmoe::Operand;
+using dsmoe::round_up;
+using dsmoe::valid_dtype;
+
+size_t esize(int t) { return t == DSMOE_F32 ? 4 : 2; }
+bool rows_ok(int64_t n) { return n >= 0 && n <= kI32Max; }
+bool dim_ok(int64_t n) { return n >= 1 && n <= DSMOE_DENSE_MAX_DIM; }
+bool half_dim_ok(int64_t n) { return n >= 1 && n <= DSMOE_DENSE_MAX_DIM / 2; }
+// a row stride, looked at only where its matrix is given
+bool ld_ok(const void* p, int64_t ld, int64_t cols) { return !p || (ld >= cols && ld <= DSMOE_DENSE_MAX_DIM); }
+bool el_aligned(const void* p, int t) { return !p || aligned(p, esize(t)); }
+bool act_ok(int act) { return act >= DSMOE_ACT_NONE && act <= DSMOE_ACT_RELU; }
+Operand operand(const void* p, int64_t ld, bool k_rows) {
+  return Operand{static_cast<const uint16_t*>(p), ld, k_rows};
+}
+
+// Regions of a workspace, each 256-byte aligned.
+struct Carver {
+  size_t off = 0;
+  size_t take(size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  }
+};
+
+dsmoe_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return DSMOE_OK;
+  if (!ws || have < need) return DSMOE_ERR_WORKSPACE;
+  return aligned(ws, 256) ? DSMOE_OK : DSMOE_ERR_ALIGN;
+}
+
+// The products of the calls, without outputs and workspace.
+DenseGemm forward_product(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                          DenseEpi epi) {
+  DenseGemm g{};
+  g.a = operand(x, ldx, false);
+  g.b = operand(w, ldw, false);
+  g.M = M, g.N = N, g.K = K, g.epi = epi;
+  return g;
+}
+// dx [M][K] = dz [M][N] w [N][K]
+DenseGemm dx_product(const void* dz, int64_t lddz, const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
+  DenseGemm g{};
+  g.a = operand(dz, lddz, false);
+  g.b = operand(w, ldw, true);
+  g.M = M, g.N = K, g.K = N;
+  return g;
+}
+// dw [N][K] = dz [M][N]^T x [M][K]
+DenseGemm dw_product(const void* dz, int64_t lddz, const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K) {
+  DenseGemm g{};
+  g.a = operand(dz, lddz, true);
+  g.b = operand(x, ldx, true);
+  g.M = N, g.N = K, g.K = M;
+  return g;
+}
+void set_output(DenseGemm& g, void* y, int64_t ldy, int yt) {
+  g.y = y;
+  g.ldy = ldy;
+  g.y_f32 = yt == DSMOE_F32;
+}
+
+// Workspace of the two products of a backward pass, whose dz has N columns:
+// dz (when it is not dy itself), the bias partials, one product's scratch
+// (the two run one after the other).
+struct BackwardLayout {
+  size_t dz, partial, product, total;
+  int64_t lddz;
+};
+BackwardLayout backward_layout(const void* dy, int64_t lddy, bool own_dz, bool bias, const void* x, int64_t ldx,
+                               const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
+  BackwardLayout L{};
+  Carver c;
+  L.lddz = own_dz ? (N + 7) / 8 * 8 : lddy;
+  if (own_dz) {
+    L.dz = c.take(static_cast<size_t>(M) * L.lddz * 2);
+    dy = nullptr;   // the workspace's own rows are aligned
+  }
+  if (bias) L.partial = c.take(static_cast<size_t>(dsmoe::bias_partial_rows(M, N)) * N * 4);
+  const size_t a = dsmoe::dense_gemm_workspace_bytes(dx_product(dy, L.lddz, w, ldw, M, N, K));
+  const size_t b = dsmoe::dense_gemm_workspace_bytes(dw_product(dy, L.lddz, x, ldx, M, N, K));
+  L.product = c.take(a > b ? a : b);
+  L.total = c.off;
+  return L;
+}
+
+// dx and dw from dz; M = 0 leaves dx alone and clears dw
+dsmoe_status run_products(const void* dz, int64_t lddz, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                          int64_t M, int64_t N, int64_t K, void* dx, int64_t lddx, int dxt, void* dw, int64_t lddw,
+                          int dwt, void* scratch, hipStream_t st) {
+  if (M == 0) return dw ? launch_status(dsmoe::launch_zero_matrix(dw, lddw, dwt == DSMOE_F32, N, K, st)) : DSMOE_OK;
+  if (dx) {
+    DenseGemm g = dx_product(dz, lddz, w, ldw, M, N, K);
+    set_output(g, dx, lddx, dxt);
+    g.workspace = scratch;
+    const hipError_t e = dsmoe::launch_dense_gemm(g, st);
+    if (e != hipSuccess) return launch_status(e);
+  }
+  if (dw) {
+    DenseGemm g = dw_product(dz, lddz, x, ldx, M, N, K);
+    set_output(g, dw, lddw, dwt);
+    g.workspace = scratch;
+    const hipError_t e = dsmoe::launch_dense_gemm(g, st);
+    if (e != hipSuccess) return launch_status(e);
+  }
+  return DSMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dsmoe_status dsmoe_layer_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int xt,
+                              const void* gamma, const void* beta, int pt, int64_t rows, int64_t cols,
+                              float eps, void* y, int64_t ldy, void* sum, int64_t lds, float* mean,
+                              float* rstd, void* stream) {
+  if (!valid_dtype(xt) || !valid_dtype(pt)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(rows) || !dim_ok(cols) || !(eps >= 0.0f) || !std::isfinite(eps)) return DSMOE_ERR_SHAPE;
+  if (!ld_ok(x, ldx, cols) || !ld_ok(residual, ldr, cols) || !ld_ok(y, ldy, cols) || !ld_ok(sum, lds, cols))
+    return DSMOE_ERR_SHAPE;
+  if (rows == 0) return DSMOE_OK;
+  if (!x || !y) return DSMOE_ERR_NULL;
+  if (!el_aligned(x, xt) || !el_aligned(residual, xt) || !el_aligned(y, xt) || !el_aligned(sum, xt) ||
+      !el_aligned(gamma, pt) || !el_aligned(beta, pt) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return DSMOE_ERR_ALIGN;
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  const dsmoe::NormFwd p{x,    ldx,  residual, ldr, xt == DSMOE_F32, gamma, beta, pt == DSMOE_F32, rows,
+                         cols, eps, y,        ldy, sum,             lds,   mean, rstd};
+  return launch_status(dsmoe::launch_layer_norm(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t dsmoe_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!rows_ok(rows) || !dim_ok(cols)) return 0;
+  return round_up(dsmoe::layer_norm_backward_partial_floats(rows, cols) * 4, 256);
+}
+
+dsmoe_status dsmoe_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                       const void* dsum, int64_t ldds, int xt, const void* gamma, int pt,
+                                       const float* mean, const float* rstd, int64_t rows, int64_t cols,
+                                       void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(xt) || !valid_dtype(pt)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(rows) || !dim_ok(cols)) return DSMOE_ERR_SHAPE;
+  if (!ld_ok(dy, lddy, cols) || !ld_ok(x, ldx, cols) || !ld_ok(dsum, ldds, cols) || !ld_ok(dx, lddx, cols))
+    return DSMOE_ERR_SHAPE;
+  if ((dgamma == nullptr) != (dbeta == nullptr)) return DSMOE_ERR_NULL;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return DSMOE_ERR_NULL;
+  if (!el_aligned(dy, xt) || !el_aligned(x, xt) || !el_aligned(dsum, xt) || !el_aligned(dx, xt) ||
+      !el_aligned(gamma, pt) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
+    return DSMOE_ERR_ALIGN;
+  if (rows == 0 && !dgamma) return DSMOE_OK;
+  if (dgamma) {
+    const dsmoe_status ws = check_workspace(workspace, ws_bytes, dsmoe_layer_norm_backward_workspace_bytes(rows, cols));
+    if (ws != DSMOE_OK) return ws;
+  }
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  const dsmoe::NormBwd p{dy,   lddy, x,    ldx,  dsum, ldds,   xt == DSMOE_F32, gamma,
+                         pt == DSMOE_F32, mean, rstd, rows, cols, dx,     lddx,            dgamma,
+                         dbeta, dgamma ? static_cast<float*>(workspace) : nullptr};
+  return launch_status(dsmoe::launch_layer_norm_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t dsmoe_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
+                                    int64_t N, int64_t K) {
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || M == 0) return 0;
+  return dsmoe::dense_gemm_workspace_bytes(forward_product(x, ldx, w, ldw, M, N, K, DenseEpi::kLinear));
+}
+
+dsmoe_status dsmoe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, int bt,
+                          const void* residual, int64_t ldr, int act, int64_t M, int64_t N, int64_t K,
+                          void* y, int64_t ldy, int yt, void* z, int64_t ldz, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  if (!valid_dtype(yt) || !valid_dtype(bt)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act)) return DSMOE_ERR_SHAPE;
+  if (!ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(residual, ldr, N) || !ld_ok(y, ldy, N) || !ld_ok(z, ldz, N))
+    return DSMOE_ERR_SHAPE;
+  if (M == 0) return DSMOE_OK;
+  if (!x || !w || !y) return DSMOE_ERR_NULL;
+  if (!aligned(x, 2) || !aligned(w, 2) || !el_aligned(bias, bt) || !el_aligned(residual, yt) || !el_aligned(y, yt) ||
+      !el_aligned(z, yt))
+    return DSMOE_ERR_ALIGN;
+  DenseGemm g = forward_product(x, ldx, w, ldw, M, N, K, DenseEpi::kLinear);
+  const dsmoe_status ws = check_workspace(workspace, ws_bytes, dsmoe::dense_gemm_workspace_bytes(g));
+  if (ws != DSMOE_OK) return ws;
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  g.act = act;
+  g.bias = bias, g.bias_f32 = bt == DSMOE_F32;
+  g.residual = residual, g.ldr = ldr;
+  set_output(g, y, ldy, yt);
+  g.z = z, g.ldz = ldz;
+  g.workspace = workspace;
+  return launch_status(dsmoe::launch_dense_gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t dsmoe_linear_backward_workspace_bytes(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                             const void* w, int64_t ldw, int act, int64_t M, int64_t N,
+                                             int64_t K) {
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act) || M == 0) return 0;
+  return backward_layout(dy, lddy, act != DSMOE_ACT_NONE, true, x, ldx, w, ldw, M, N, K).total;
+}
+
+dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                                   int64_t ldw, const void* z, int64_t ldz, int zt, int act, int64_t M,
+                                   int64_t N, int64_t K, void* dx, int64_t lddx, int dxt, void* dw,
+                                   int64_t lddw, int dwt, float* dbias, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  if (!valid_dtype(zt) || !valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act)) return DSMOE_ERR_SHAPE;
+  const bool own_dz = act != DSMOE_ACT_NONE;
+  if (!own_dz) z = nullptr;
+  if (!ld_ok(dy, lddy, N) || !ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(z, ldz, N) || !ld_ok(dx, lddx, K) ||
+      !ld_ok(dw, lddw, K))
+    return DSMOE_ERR_SHAPE;
+  if (M > 0 && (!dy || (own_dz && !z) || (dx && !w) || (dw && !x))) return DSMOE_ERR_NULL;
+  if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(w, 2) || !el_aligned(z, zt) || !el_aligned(dx, dxt) ||
+      !el_aligned(dw, dwt) || !aligned(dbias, 4))
+    return DSMOE_ERR_ALIGN;
+  if (!dx && !dw && !dbias) return DSMOE_OK;
+  if (M == 0 && !dw && !dbias) return DSMOE_OK;
+  const BackwardLayout L = backward_layout(dy, lddy, own_dz, true, x, ldx, w, ldw, M, N, K);
+  if (M > 0) {
+    const dsmoe_status ws = check_workspace(workspace, ws_bytes, L.total);
+    if (ws != DSMOE_OK) return ws;
+  }
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const uint16_t* dz = static_cast<const uint16_t*>(dy);
+  if (M == 0) {
+    if (dbias) {
+      const hipError_t e = dsmoe::launch_zero_matrix(dbias, N, true, 1, N, st);
+      if (e != hipSuccess) return launch_status(e);
+    }
+  } else if (dbias || own_dz) {
+    uint16_t* to = own_dz && (dx || dw) ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
+    float* partial = dbias ? reinterpret_cast<float*>(base + L.partial) : nullptr;
+    hipError_t e = dsmoe::launch_act_backward(dz, lddy, z, ldz, zt == DSMOE_F32, act, M, N, to, L.lddz, partial, st);
+    if (e == hipSuccess && dbias)
+      e = dsmoe::launch_sum_partials(partial, dsmoe::bias_partial_rows(M, N), N, dbias, st);
+    if (e != hipSuccess) return launch_status(e);
+    if (to) dz = to;
+  }
+  return run_products(dz, L.lddz, x, ldx, w, ldw, M, N, K, dx, lddx, dxt, dw, lddw, dwt, base + L.product, st);
+}
+
+size_t dsmoe_gated_linear_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw, int64_t M,
+                                          int64_t H, int64_t I) {
+  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || M == 0) return 0;
+  return dsmoe::dense_gemm_workspace_bytes(forward_product(x, ldx, w13, ldw, M, I, H, DenseEpi::kGated));
+}
+
+dsmoe_status dsmoe_gated_linear(const void* x, int64_t ldx, const void* w13, int64_t ldw, int act, int64_t M,
+                                int64_t H, int64_t I, void* a, int64_t lda, int at, void* h, int64_t ldh,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(at)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || !act_ok(act)) return DSMOE_ERR_SHAPE;
+  if (!ld_ok(x, ldx, H) || !ld_ok(w13, ldw, H) || !ld_ok(a, lda, I) || !ld_ok(h, ldh, 2 * I)) return DSMOE_ERR_SHAPE;
+  if (M == 0) return DSMOE_OK;
+  if (!x || !w13 || !a) return DSMOE_ERR_NULL;
+  if (!aligned(x, 2) || !aligned(w13, 2) || !el_aligned(a, at) || !aligned(h, 2)) return DSMOE_ERR_ALIGN;
+  DenseGemm g = forward_product(x, ldx, w13, ldw, M, I, H, DenseEpi::kGated);
+  const dsmoe_status ws = check_workspace(workspace, ws_bytes, dsmoe::dense_gemm_workspace_bytes(g));
+  if (ws != DSMOE_OK) return ws;
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  g.act = act;
+  set_output(g, a, lda, at);
+  g.z = h, g.ldz = ldh;
+  g.workspace = workspace;
+  return launch_status(dsmoe::launch_dense_gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t dsmoe_gated_linear_backward_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw,
+                                                   int64_t M, int64_t H, int64_t I) {
+  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || M == 0) return 0;
+  return backward_layout(nullptr, 0, true, false, x, ldx, w13, ldw, M, 2 * I, H).total;
+}
+
+dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const void* x, int64_t ldx,
+                                         const void* w13, int64_t ldw, const void* h, int64_t ldh, int act,
+                                         int64_t M, int64_t H, int64_t I, void* dx, int64_t lddx, int dxt,
+                                         void* dw13, int64_t lddw, int dwt, void* workspace, size_t ws_bytes,
+                                         void* stream) {
+  if (!valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
+  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || !act_ok(act)) return DSMOE_ERR_SHAPE;
+  if (!ld_ok(da, ldda, I) || !ld_ok(x, ldx, H) || !ld_ok(w13, ldw, H) || !ld_ok(h, ldh, 2 * I) ||
+      !ld_ok(dx, lddx, H) || !ld_ok(dw13, lddw, H))
+    return DSMOE_ERR_SHAPE;
+  if (M > 0 && (!da || !h || (dx && !w13) || (dw13 && !x))) return DSMOE_ERR_NULL;
+  if (!aligned(da, 2) || !aligned(x, 2) || !aligned(w13, 2) || !aligned(h, 2) || !el_aligned(dx, dxt) ||
+      !el_aligned(dw13, dwt))
+    return DSMOE_ERR_ALIGN;
+  if ((!dx && !dw13) || (M == 0 && !dw13)) return DSMOE_OK;
+  const BackwardLayout L = backward_layout(nullptr, 0, true, false, x, ldx, w13, ldw, M, 2 * I, H);
+  if (M > 0) {
+    const dsmoe_status ws = check_workspace(workspace, ws_bytes, L.total);
+    if (ws != DSMOE_OK) return ws;
+  }
+  const dsmoe_status ds = check_device();
+  if (ds != DSMOE_OK) return ds;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(base + L.dz);
+  const hipError_t e = dsmoe::launch_gated_backward(static_cast<const uint16_t*>(da), ldda,
+                                                    static_cast<const uint16_t*>(h), ldh, act, M, I, dh, L.lddz, st);
+  if (e != hipSuccess) return launch_status(e);
+  return run_products(dh, L.lddz, x, ldx, w13, ldw, M, 2 * I, H, dx, lddx, dxt, dw13, lddw, dwt, base + L.product, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,173 @@
+// Elementwise parts of the dense backward passes: the gradient at the
+// pre-activations, rounded to bf16 once as the operand of the two products
+// that follow, and the bias gradient's column sums (of the unrounded values).
+// HBM bounds them: dy and z (or da and h) in, dz (dh) out.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "act.h"
+#include "common.h"
+#include "dense.h"
+
+namespace dsmoe {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 8 columns of a row from column c (c < n): one 16-byte access per 16 bytes
+// when vec (n a multiple of 8 and the row 16-byte aligned), else one by one,
+// 0 past the row's end
+template <bool F32>
+__device__ __forceinline__ void load8(const void* row, int64_t c, int64_t n, bool vec, float* o) {
+  if (vec) {
+    if constexpr (F32) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
+      const f32x4 a = q[0], b = q[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
+    } else {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[2 * e] = __uint_as_float(a[e] << 16);
+        o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (F32)
+        o[e] = c + e < n ? static_cast<const float*>(row)[c + e] : 0.0f;
+      else
+        o[e] = c + e < n ? bf16_to_f32(static_cast<const uint16_t*>(row)[c + e]) : 0.0f;
+    }
+  }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float* v) {
+  u32x4 a;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+  return a;
+}
+
+// Block (x, y): 256 slots of 8 columns, strip y of the rows.
+template <bool ZF32>
+__global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
+                                                           const void* __restrict__ z, int64_t ldz, bool vec,
+                                                           int act, int64_t M, int64_t N, int64_t strip,
+                                                           uint16_t* __restrict__ dz, int64_t lddz,
+                                                           float* __restrict__ partial) {
+  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
+  if (c >= N) return;
+  float sum[8] = {};
+  const int64_t r1 = min(M, (blockIdx.y + 1) * strip);
+  for (int64_t r = blockIdx.y * strip; r < r1; ++r) {
+    float g[8];
+    load8<false>(dy + r * lddy, c, N, vec, g);
+    if (z) {
+      float zz[8];
+      load8<ZF32>(static_cast<const char*>(z) + r * ldz * (ZF32 ? 4 : 2), c, N, vec, zz);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f, d;
+        act_and_grad_f32(act, zz[e], f, d);
+        g[e] *= d;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += g[e];
+    // dz's rows are padded to a multiple of 8 with zeros (the products read
+    // whole groups of 8)
+    if (dz) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e >= N) g[e] = 0.0f;
+      *reinterpret_cast<u32x4*>(dz + r * lddz + c) = pack8(g);
+    }
+  }
+  if (partial) {
+    float* o = partial + blockIdx.y * N + c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < N) o[e] = sum[e];
+  }
+}
+
+// Block (x, y): 256 slots of 8 columns of da, strip y of the rows.
+__global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __restrict__ da, int64_t ldda,
+                                                             const uint16_t* __restrict__ h, int64_t ldh, bool vec,
+                                                             int act, int64_t M, int64_t I, int64_t strip,
+                                                             uint16_t* __restrict__ dh, int64_t lddh) {
+  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
+  if (c >= I) return;
+  const int64_t r1 = min(M, (blockIdx.y + 1) * strip);
+  for (int64_t r = blockIdx.y * strip; r < r1; ++r) {
+    float d[8], g[8], u[8], dg[8], du[8];
+    load8<false>(da + r * ldda, c, I, vec, d);
+    load8<false>(h + r * ldh, c, I, vec, g);
+    load8<false>(h + r * ldh + I, c, I, vec, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float f, df;
+      act_and_grad_f32(act, g[e], f, df);
+      dg[e] = d[e] * u[e] * df;
+      du[e] = d[e] * f;
+    }
+    uint16_t* o = dh + r * lddh + c;
+    if (vec) {
+      *reinterpret_cast<u32x4*>(o) = pack8(dg);
+      *reinterpret_cast<u32x4*>(o + I) = pack8(du);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < I) {
+          o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
+          o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
+        }
+      // the row's padding past 2 I, by the thread that owns the last column
+      if (c + 8 >= I)
+        for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
+    }
+  }
+}
+
+bool row16(const void* p, int64_t ld, int es) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
+}
+
+// rows per strip: 16 or more, with at most 256 strips
+int64_t strip_rows(int64_t M) {
+  const int64_t s = (M + 255) / 256;
+  return s < 16 ? 16 : s;
+}
+
+}  // namespace
+
+int64_t bias_partial_rows(int64_t M, int64_t N) { return M == 0 ? 0 : (M + strip_rows(M) - 1) / strip_rows(M); }
+
+hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz, bool z_f32, int act,
+                               int64_t M, int64_t N, uint16_t* dz, int64_t lddz, float* partial, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  const bool vec = N % 8 == 0 && row16(dy, lddy, 2) && row16(z, ldz, z_f32 ? 4 : 2);
+  const int64_t strip = strip_rows(M);
+  const dim3 grid(static_cast<uint32_t>((N + 2047) / 2048), static_cast<uint32_t>((M + strip - 1) / strip));
+  if (z_f32)
+    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, strip, dz, lddz, partial);
+  else
+    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, strip, dz, lddz, partial);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_t* h, int64_t ldh, int act,
+                                 int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  const bool vec = I % 8 == 0 && row16(da, ldda, 2) && row16(h, ldh, 2);
+  const int64_t strip = strip_rows(M);
+  const dim3 grid(static_cast<uint32_t>((I + 2047) / 2048), static_cast<uint32_t>((M + strip - 1) / strip));
+  gated_backward_kernel<<<grid, 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, strip, dh, lddh);
+  return hipGetLastError();
+}
+
+}  // namespace dsmoe

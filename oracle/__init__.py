@@ -31,6 +31,7 @@ gemm   -- block-scaled FP8 GEMM with per-128-K promotion (float64)
 route  -- sigmoid affinity, bias-adjusted group-limited top-K, gates, permute
 layer  -- expert SwiGLU FFN and the whole MoE layer forward
 bias   -- auxiliary-loss-free bias update
+dense  -- dense feed-forward operators: layer norm, linear, gated linear (definitions)
 """
 
 from . import e4m3, quant, gemm, route, layer, bias  # noqa: F401
