@@ -61,7 +61,10 @@ struct Operand {
   const uint16_t* p;
   int64_t ld;
   bool k_rows;
+  bool padded;            // rows are readable, and zero, up to a multiple of 8 values
 };
+// whether a row of `cols` values is made of whole aligned groups of 8
+bool operand_copyable(const Operand& o, int64_t cols);
 
 enum class DenseEpi : int {
   kLinear = 0,   // z = acc + bias, y = act(z) + residual

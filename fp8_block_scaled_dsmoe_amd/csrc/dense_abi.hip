@@ -29,8 +29,8 @@ bool half_dim_ok(int64_t n) { return n >= 1 && n <= DSMOE_DENSE_MAX_DIM / 2; }
 bool ld_ok(const void* p, int64_t ld, int64_t cols) { return !p || (ld >= cols && ld <= DSMOE_DENSE_MAX_DIM); }
 bool el_aligned(const void* p, int t) { return !p || aligned(p, esize(t)); }
 bool act_ok(int act) { return act >= DSMOE_ACT_NONE && act <= DSMOE_ACT_RELU; }
-Operand operand(const void* p, int64_t ld, bool k_rows) {
-  return Operand{static_cast<const uint16_t*>(p), ld, k_rows};
+Operand operand(const void* p, int64_t ld, bool k_rows, bool padded = false) {
+  return Operand{static_cast<const uint16_t*>(p), ld, k_rows, padded};
 }
 
 // Regions of a workspace, each 256-byte aligned.
@@ -59,17 +59,17 @@ DenseGemm forward_product(const void* x, int64_t ldx, const void* w, int64_t ldw
   return g;
 }
 // dx [M][K] = dz [M][N] w [N][K]
-DenseGemm dx_product(const void* dz, int64_t lddz, const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
+DenseGemm dx_product(const void* dz, int64_t lddz, bool padded, const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
   DenseGemm g{};
-  g.a = operand(dz, lddz, false);
+  g.a = operand(dz, lddz, false, padded);
   g.b = operand(w, ldw, true);
   g.M = M, g.N = K, g.K = N;
   return g;
 }
 // dw [N][K] = dz [M][N]^T x [M][K]
-DenseGemm dw_product(const void* dz, int64_t lddz, const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K) {
+DenseGemm dw_product(const void* dz, int64_t lddz, bool padded, const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K) {
   DenseGemm g{};
-  g.a = operand(dz, lddz, true);
+  g.a = operand(dz, lddz, true, padded);
   g.b = operand(x, ldx, true);
   g.M = N, g.N = K, g.K = M;
   return g;
@@ -81,43 +81,47 @@ void set_output(DenseGemm& g, void* y, int64_t ldy, int yt) {
 }
 
 // Workspace of the two products of a backward pass, whose dz has N columns:
-// dz (when it is not dy itself), the bias partials, one product's scratch
-// (the two run one after the other).
+// dz (when it is not dy itself: an activation, or rows the products cannot
+// copy), the bias partials, one product's scratch (the two run one after the
+// other).
 struct BackwardLayout {
   size_t dz, partial, product, total;
   int64_t lddz;
+  bool own_dz;
 };
-BackwardLayout backward_layout(const void* dy, int64_t lddy, bool own_dz, bool bias, const void* x, int64_t ldx,
+BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool bias, const void* x, int64_t ldx,
                                const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
   BackwardLayout L{};
+  if (M == 0) return L;
   Carver c;
+  const bool own_dz = L.own_dz = act || !dsmoe::operand_copyable(operand(dy, lddy, false), N);
   L.lddz = own_dz ? (N + 7) / 8 * 8 : lddy;
   if (own_dz) {
     L.dz = c.take(static_cast<size_t>(M) * L.lddz * 2);
     dy = nullptr;   // the workspace's own rows are aligned
   }
   if (bias) L.partial = c.take(static_cast<size_t>(dsmoe::bias_partial_rows(M, N)) * N * 4);
-  const size_t a = dsmoe::dense_gemm_workspace_bytes(dx_product(dy, L.lddz, w, ldw, M, N, K));
-  const size_t b = dsmoe::dense_gemm_workspace_bytes(dw_product(dy, L.lddz, x, ldx, M, N, K));
+  const size_t a = dsmoe::dense_gemm_workspace_bytes(dx_product(dy, L.lddz, own_dz, w, ldw, M, N, K));
+  const size_t b = dsmoe::dense_gemm_workspace_bytes(dw_product(dy, L.lddz, own_dz, x, ldx, M, N, K));
   L.product = c.take(a > b ? a : b);
   L.total = c.off;
   return L;
 }
 
 // dx and dw from dz; M = 0 leaves dx alone and clears dw
-dsmoe_status run_products(const void* dz, int64_t lddz, const void* x, int64_t ldx, const void* w, int64_t ldw,
+dsmoe_status run_products(const void* dz, int64_t lddz, bool padded, const void* x, int64_t ldx, const void* w, int64_t ldw,
                           int64_t M, int64_t N, int64_t K, void* dx, int64_t lddx, int dxt, void* dw, int64_t lddw,
                           int dwt, void* scratch, hipStream_t st) {
   if (M == 0) return dw ? launch_status(dsmoe::launch_zero_matrix(dw, lddw, dwt == DSMOE_F32, N, K, st)) : DSMOE_OK;
   if (dx) {
-    DenseGemm g = dx_product(dz, lddz, w, ldw, M, N, K);
+    DenseGemm g = dx_product(dz, lddz, padded, w, ldw, M, N, K);
     set_output(g, dx, lddx, dxt);
     g.workspace = scratch;
     const hipError_t e = dsmoe::launch_dense_gemm(g, st);
     if (e != hipSuccess) return launch_status(e);
   }
   if (dw) {
-    DenseGemm g = dw_product(dz, lddz, x, ldx, M, N, K);
+    DenseGemm g = dw_product(dz, lddz, padded, x, ldx, M, N, K);
     set_output(g, dw, lddw, dwt);
     g.workspace = scratch;
     const hipError_t e = dsmoe::launch_dense_gemm(g, st);
@@ -229,18 +233,18 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
                                    void* stream) {
   if (!valid_dtype(zt) || !valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
   if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act)) return DSMOE_ERR_SHAPE;
-  const bool own_dz = act != DSMOE_ACT_NONE;
-  if (!own_dz) z = nullptr;
+  const bool has_act = act != DSMOE_ACT_NONE;
+  if (!has_act) z = nullptr;
   if (!ld_ok(dy, lddy, N) || !ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(z, ldz, N) || !ld_ok(dx, lddx, K) ||
       !ld_ok(dw, lddw, K))
     return DSMOE_ERR_SHAPE;
-  if (M > 0 && (!dy || (own_dz && !z) || (dx && !w) || (dw && !x))) return DSMOE_ERR_NULL;
+  if (M > 0 && (!dy || (has_act && !z) || (dx && !w) || (dw && !x))) return DSMOE_ERR_NULL;
   if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(w, 2) || !el_aligned(z, zt) || !el_aligned(dx, dxt) ||
       !el_aligned(dw, dwt) || !aligned(dbias, 4))
     return DSMOE_ERR_ALIGN;
   if (!dx && !dw && !dbias) return DSMOE_OK;
   if (M == 0 && !dw && !dbias) return DSMOE_OK;
-  const BackwardLayout L = backward_layout(dy, lddy, own_dz, true, x, ldx, w, ldw, M, N, K);
+  const BackwardLayout L = backward_layout(dy, lddy, has_act, true, x, ldx, w, ldw, M, N, K);
   if (M > 0) {
     const dsmoe_status ws = check_workspace(workspace, ws_bytes, L.total);
     if (ws != DSMOE_OK) return ws;
@@ -255,8 +259,8 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
       const hipError_t e = dsmoe::launch_zero_matrix(dbias, N, true, 1, N, st);
       if (e != hipSuccess) return launch_status(e);
     }
-  } else if (dbias || own_dz) {
-    uint16_t* to = own_dz && (dx || dw) ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
+  } else if (dbias || L.own_dz) {
+    uint16_t* to = L.own_dz && (dx || dw) ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
     float* partial = dbias ? reinterpret_cast<float*>(base + L.partial) : nullptr;
     hipError_t e = dsmoe::launch_act_backward(dz, lddy, z, ldz, zt == DSMOE_F32, act, M, N, to, L.lddz, partial, st);
     if (e == hipSuccess && dbias)
@@ -264,7 +268,7 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
     if (e != hipSuccess) return launch_status(e);
     if (to) dz = to;
   }
-  return run_products(dz, L.lddz, x, ldx, w, ldw, M, N, K, dx, lddx, dxt, dw, lddw, dwt, base + L.product, st);
+  return run_products(dz, L.lddz, L.own_dz, x, ldx, w, ldw, M, N, K, dx, lddx, dxt, dw, lddw, dwt, base + L.product, st);
 }
 
 size_t dsmoe_gated_linear_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw, int64_t M,
@@ -328,7 +332,7 @@ dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const voi
   const hipError_t e = dsmoe::launch_gated_backward(static_cast<const uint16_t*>(da), ldda,
                                                     static_cast<const uint16_t*>(h), ldh, act, M, I, dh, L.lddz, st);
   if (e != hipSuccess) return launch_status(e);
-  return run_products(dh, L.lddz, x, ldx, w13, ldw, M, 2 * I, H, dx, lddx, dxt, dw13, lddw, dwt, base + L.product, st);
+  return run_products(dh, L.lddz, true, x, ldx, w13, ldw, M, 2 * I, H, dx, lddx, dxt, dw13, lddw, dwt, base + L.product, st);
 }
 
 }  // extern "C"

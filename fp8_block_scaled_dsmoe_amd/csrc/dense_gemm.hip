@@ -1,7 +1,19 @@
 // Matrix products of the dense feed-forward operators in bf16 with float32
 // sums: c[m][n] = sum_k a(m, k) b(n, k) and a fused epilogue.  Either operand
-// may be stored with the contraction index along its rows (forward: x and W;
-// dx: dz) or across them (dx: W; dW: dz and x).
+// may be stored with the contraction index along its rows ("row" operands:
+// x and W forward, dz in dx) or across them ("k-row" operands: W in dx, dz
+// and x in dW).
+//
+// One kernel, dense_tile_kernel, in several tile shapes.  A block computes a
+// BM x BN tile in steps of 64 of K ("chunks").  Both operand tiles are split
+// in two halves (rows [0, BM/2) and [BM/2, BM), and so for B), and every wave
+// owns an equal part of each half, so that a chunk falls into four phases,
+//     (A0 B0) (A0 B1) (A1 B1) (A1 B0),
+// each a quarter of the tile's multiply-adds that needs one new half (two in
+// the first) read from LDS into registers.  Once every wave has read a half,
+// its place in LDS is refilled with the same half of the chunk two ahead by
+// asynchronous copies (buffer loads straight to LDS), one half per phase: the
+// copies have six phases to arrive, and only two chunks are ever in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -13,117 +25,717 @@ namespace dsmoe {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ float load1(const void* p, int64_t i, bool f32) {
-  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
-__device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float v) {
-  if (f32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(f32x2_to_bf16x2(v, 0.0f));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+#define DSMOE_LDS __attribute__((address_space(3)))
+template <typename T>
+__device__ __forceinline__ DSMOE_LDS T* lds_ptr(uint32_t at) {
+  return (DSMOE_LDS T*)static_cast<uintptr_t>(at);
 }
 
-// One result (m, n) of the linear epilogue.
-__device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int64_t n, float acc) {
-  if (p.bias) acc += load1(p.bias, n, p.bias_f32);
-  if (p.z) store1(p.z, m * p.ldz + n, p.y_f32, acc);
-  float y = act_f32(p.act, acc);
-  if (p.residual) y += load1(p.residual, m * p.ldr + n, p.y_f32);
-  store1(p.y, m * p.ldy + n, p.y_f32, y);
-}
-// One result (m, n) of the gated epilogue, from its gate and up sums.
-__device__ __forceinline__ void finish_gated(const DenseGemm& p, int64_t m, int64_t n, float g, float u) {
-  if (p.z) {
-    store1(p.z, m * p.ldz + n, false, g);
-    store1(p.z, m * p.ldz + p.N + n, false, u);
-  }
-  store1(p.y, m * p.ldy + n, p.y_f32, act_f32(p.act, g) * u);
-}
+constexpr int kChunk = 64;   // K per chunk
+constexpr int kXcds = 8;
 
-// 64 x 64 tile (kGated: 32 gate and the same 32 up columns), 4 waves of
-// 32 x 32 by v_mfma_f32_16x16x32_bf16, one 32-deep step of K in LDS at a time.
-constexpr int kRowPad = 40;   // LDS row of 32 values, 80 bytes apart
-template <DenseEpi EPI>
-__global__ __launch_bounds__(256) void dense_gemm_kernel(DenseGemm p) {
-  constexpr bool kGated = EPI == DenseEpi::kGated;
-  constexpr int BN = kGated ? 32 : 64;   // result columns of the tile
-  __shared__ __attribute__((aligned(16))) uint16_t s_a[64 * kRowPad], s_b[64 * kRowPad];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t tiles_n = (p.N + BN - 1) / BN;
-  const int64_t m0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * BN;
-  f32x4 acc[2][2] = {};
-  for (int64_t k0 = 0; k0 < p.K; k0 += 32) {
-    for (int i = tid; i < 64 * 32; i += 256) {
-      // consecutive threads along the operand's contiguous index
-      const int ra = p.a.k_rows ? i & 63 : i >> 5, ka = p.a.k_rows ? i >> 6 : i & 31;
-      const int64_t m = m0 + ra, k = k0 + ka;
-      s_a[ra * kRowPad + ka] =
-          m < p.M && k < p.K ? p.a.p[p.a.k_rows ? k * p.a.ld + m : m * p.a.ld + k] : static_cast<uint16_t>(0);
-      const int rb = p.b.k_rows ? i & 63 : i >> 5, kb = p.b.k_rows ? i >> 6 : i & 31;
-      const int64_t nn = n0 + (kGated ? rb & 31 : rb), kk = k0 + kb;
-      const int64_t n = kGated && rb >= 32 ? p.N + nn : nn;
-      s_b[rb * kRowPad + kb] =
-          nn < p.N && kk < p.K ? p.b.p[p.b.k_rows ? kk * p.b.ld + n : n * p.b.ld + kk] : static_cast<uint16_t>(0);
+// ---------------------------------------------------------------------------
+// Epilogue: W (4 or 8) adjacent columns of one row.
+// ---------------------------------------------------------------------------
+
+// columns i .. i + W - 1 of a row at base (f32 or bf16); valid of them exist.
+// vec: i-th element 4 W (2 W) byte aligned and all W exist.
+template <int W>
+__device__ __forceinline__ void load_cols(const void* base, int64_t i, bool f32, bool vec, int valid, float* o) {
+  if (f32) {
+    const float* q = static_cast<const float*>(base) + i;
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < W; j += 4) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(q + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j + e] = a[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) o[e] = e < valid ? q[e] : 0.0f;
     }
-    __syncthreads();
-    // operand lane l: row l % 16, k = 8 (l / 16) + [0, 8)
-    bf16x8 fa[2], fb[2];
-    const int r = lane & 15, q = (lane >> 4) * 8;
+  } else {
+    const uint16_t* q = static_cast<const uint16_t*>(base) + i;
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int ra = 32 * (wave >> 1) + 16 * i + r;
-      // kGated: b fragment 0 holds gate columns, fragment 1 the same up columns
-      const int rb = kGated ? 32 * i + 16 * (wave & 1) + r : 32 * (wave & 1) + 16 * i + r;
-      fa[i] = *reinterpret_cast<const bf16x8*>(&s_a[ra * kRowPad + q]);
-      fb[i] = *reinterpret_cast<const bf16x8*>(&s_b[rb * kRowPad + q]);
-    }
+      for (int j = 0; j < W; j += 4) {
+        const u32x2 a = *reinterpret_cast<const u32x2*>(q + j);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    __syncthreads();
-  }
-  // result lane l: row l % 16 of a, columns 4 (l / 16) + [0, 4) of b
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if constexpr (kGated) {
-        const int64_t n = n0 + 16 * (wave & 1) + 4 * (lane >> 4) + r;
-        if (n < p.N) finish_gated(p, m, n, acc[i][0][r], acc[i][1][r]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t n = n0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4) + r;
-          if (n < p.N) finish_linear(p, m, n, acc[i][j][r]);
+        for (int e = 0; e < 2; ++e) {
+          o[j + 2 * e] = __uint_as_float(a[e] << 16);
+          o[j + 2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
         }
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) o[e] = e < valid ? bf16_to_f32(q[e]) : 0.0f;
     }
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_cols(void* base, int64_t i, bool f32, bool vec, int valid, const float* v) {
+  if (f32) {
+    float* q = static_cast<float*>(base) + i;
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < W; j += 4) *reinterpret_cast<f32x4*>(q + j) = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if (e < valid) q[e] = v[e];
+    }
+  } else {
+    uint16_t* q = static_cast<uint16_t*>(base) + i;
+    if (vec) {
+      uint32_t a[W / 2];
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+      if constexpr (W == 8)
+        *reinterpret_cast<u32x4*>(q) = u32x4{a[0], a[1], a[2], a[3]};
+      else
+        *reinterpret_cast<u32x2*>(q) = u32x2{a[0], a[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if (e < valid) q[e] = static_cast<uint16_t>(f32x2_to_bf16x2(v[e], 0.0f));
+    }
+  }
+}
+
+struct TileArgs {
+  DenseGemm p;
+  int64_t a_k, b_k;       // contraction length readable along a row (row operands: a multiple of 8)
+  int64_t a_r, b_r;       // rows readable (k-row operands: a multiple of 8; kGated: of one half of b)
+  bool vec;               // every matrix of the epilogue takes vector accesses
+  float* partial;         // splits > 1: [split][M][ldp] partial sums, no epilogue
+  int64_t ldp;            // (kGated: gate sums, then up sums at + N rounded up to 8)
+  int32_t splits;
+  int32_t chunks;         // chunks of K in all
+  int32_t tiles_m, tiles_n;
+};
+
+// y = act(acc + bias) + residual, z = acc + bias
+template <int W>
+__device__ __forceinline__ void finish_linear(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* v,
+                                              const float* bias) {
+  const int valid = static_cast<int>(min(static_cast<int64_t>(W), p.N - n));
+  const bool vec = pvec && valid == W;
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] += bias[e];
+  if (p.z) store_cols<W>(p.z, m * p.ldz + n, p.y_f32, vec, valid, v);
+  if (p.act != DSMOE_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = act_f32(p.act, v[e]);
+  }
+  if (p.residual) {
+    float r[W];
+    load_cols<W>(p.residual, m * p.ldr + n, p.y_f32, vec, valid, r);
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] += r[e];
+  }
+  store_cols<W>(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+}
+
+// a = act(g) u, h = [g | u]
+template <int W>
+__device__ __forceinline__ void finish_gated(const DenseGemm& p, bool pvec, int64_t m, int64_t n, const float* g,
+                                             const float* u) {
+  const int valid = static_cast<int>(min(static_cast<int64_t>(W), p.N - n));
+  const bool vec = pvec && valid == W;
+  if (p.z) {
+    store_cols<W>(p.z, m * p.ldz + n, false, vec, valid, g);
+    store_cols<W>(p.z, m * p.ldz + p.N + n, false, vec, valid, u);
+  }
+  float v[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = act_f32(p.act, g[e]) * u[e];
+  store_cols<W>(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+}
+
+template <int W>
+__device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* o) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    o[e] = 0.0f;
+    if (p.bias && n + e < p.N)
+      o[e] = p.bias_f32 ? static_cast<const float*>(p.bias)[n + e]
+                        : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n + e]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Operand halves: from memory to LDS, from LDS to MFMA operands.
+// ---------------------------------------------------------------------------
+
+// Asynchronous copy of 16 bytes per lane to lds + 16 lane (wave-uniform lds):
+// offset voff from the resource's base; past its range zeros are written.
+// Issued from assembly so that the compiler neither waits for it nor counts
+// it; the kernel waits for vmcnt itself.
+__device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  static_assert(N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// One half (HR rows x 64 of K) of an operand tile in LDS, HR * 128 bytes.
+//
+// Row operand: row r is 128 bytes of 8 16-byte segments, segment s stored in
+// place s ^ (r % 8), so that the 16 rows an operand read touches at one
+// segment spread over all banks.
+// K-row operand: k is a row of HR * 2 bytes of HR / 16 32-byte blocks (16
+// columns), block b stored in place b ^ key(k); operands are read with the
+// transposing LDS read, which takes four rows of k x 16 columns per 16 lanes
+// and gives each lane its column: the key separates the rows that one read
+// touches.
+template <int HR, bool KROWS, int NW>
+struct Half {
+  static constexpr int kBytes = HR * 128;
+  static constexpr int kCopies = HR / (8 * NW);       // copies per wave and half
+  static_assert(HR % (8 * NW) == 0, "whole copies");
+  static constexpr int kSegs = HR / 8;                // k-row operand: 16-byte segments of a row
+  static constexpr int kRows = 64 / kSegs;            // rows of k per copy
+
+  static __device__ __forceinline__ int key(int k) {
+    if constexpr (HR == 128) return (k & 3) | ((k >> 3) & 1) << 2;
+    if constexpr (HR == 64) return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+    return (k >> 3) & 1;
+  }
+};
+
+// Where a wave's copies of one half read: a resource that starts at the
+// half's chunk and ends with the last valid element, moved on by advance().
+template <int HR, bool KROWS, int NW>
+struct Source {
+  using H = Half<HR, KROWS, NW>;
+  uint64_t base;          // byte address of the half's (row 0, chunk's first k)
+  int64_t step;           // bytes per chunk
+  int64_t range;          // row operand: valid bytes from base; k-row operand: bytes of the valid columns of a row
+  uint32_t ld2;           // row stride in bytes
+  int32_t k_left;         // valid k from base on
+
+  // rows [r0, r0 + HR) of the operand, chunks from k0 on, k_end: end of valid k
+  __device__ __forceinline__ Source(const Operand& o, int64_t r0, int64_t rows, int64_t k0, int64_t k_end) {
+    ld2 = static_cast<uint32_t>(o.ld * 2);
+    const int64_t left = min(static_cast<int64_t>(HR), rows - r0);
+    k_left = static_cast<int32_t>(k_end - k0);
+    if constexpr (KROWS) {
+      base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(k0 * o.ld + r0) * 2;
+      step = static_cast<int64_t>(ld2) * kChunk;
+      range = left > 0 ? left * 2 : 0;
+    } else {
+      base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(r0 * o.ld + k0) * 2;
+      step = kChunk * 2;
+      range = left > 0 ? (left - 1) * static_cast<int64_t>(ld2) + 2 * static_cast<int64_t>(k_left) : 0;
+    }
+    if (left <= 0) k_left = 0;
+  }
+  __device__ __forceinline__ i32x4 resource() const {
+    int64_t n = 0;
+    if (k_left > 0) {
+      if constexpr (KROWS)
+        n = static_cast<int64_t>(min(k_left, kChunk) - 1) * ld2 + range;
+      else
+        n = range;
+    }
+    i32x4 r;
+    r.x = __builtin_amdgcn_readfirstlane(static_cast<int>(base & 0xffffffffu));
+    r.y = __builtin_amdgcn_readfirstlane(static_cast<int>((base >> 32) & 0xffffu));   // raw buffer: stride 0
+    r.z = __builtin_amdgcn_readfirstlane(static_cast<int>(n));
+    r.w = 0x00020000;
+    return r;
+  }
+  // Issue this wave's copies of the current chunk to the half at lds, move on.
+  // voff: the lane's offsets (lane_offsets); lane_k: the first k of its
+  // segment (row operand).
+  __device__ __forceinline__ void copy(const uint32_t (&voff)[H::kCopies], int lane_k, uint32_t lds, int wave) {
+    const i32x4 rs = resource();
+#pragma unroll
+    for (int i = 0; i < H::kCopies; ++i) {
+      // a segment past the row's last valid k would read the next row
+      const uint32_t v = KROWS || lane_k < k_left ? voff[i] : 0x80000000u;
+      copy16(rs, v, __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
+    }
+    base += step;
+    if constexpr (!KROWS) range -= 2 * kChunk;
+    k_left -= kChunk;
+  }
+  // The lane's byte offsets from base; cols_left: valid columns (k-row operand).
+  static __device__ __forceinline__ void lane_offsets(uint32_t (&voff)[H::kCopies], uint32_t ld2, int64_t cols_left,
+                                                      int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < H::kCopies; ++i) {
+      const int j = wave * H::kCopies + i;
+      if constexpr (KROWS) {
+        const int k = j * H::kRows + lane / H::kSegs, seg = lane % H::kSegs;
+        const int col = ((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8;
+        voff[i] = col < cols_left ? static_cast<uint32_t>(k) * ld2 + col * 2 : 0x80000000u;
+      } else {
+        voff[i] = static_cast<uint32_t>(8 * j + lane / 8) * ld2 + (((lane & 7) ^ (lane >> 3)) << 4);
+      }
+    }
+  }
+};
+
+// A wave's reader of T 16-row operand fragments from row0 of a half:
+// fragment i, K step kk (of 2): lane l holds row l % 16, k = 32 kk + 8 (l / 16)
+// + [0, 8).
+template <int HR, bool KROWS, int T>
+struct Reader {
+  uint32_t at[KROWS ? T : 2];
+  __device__ __forceinline__ Reader(int row0, int lane) {
+    if constexpr (KROWS) {
+      const int s = lane & 15, g = lane >> 4;
+      const int k = 8 * g + (s >> 2);      // key() ignores the bits the reads below add to k
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+        at[i] = k * HR * 2 + (((row0 / 16 + i) ^ Half<HR, true, 1>::key(k)) << 5) + (s & 3) * 8;
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        at[kk] = (row0 + (lane & 15)) * 128 + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
+    }
+  }
+  __device__ __forceinline__ bf16x8 read(uint32_t half, int i, int kk) const {
+    if constexpr (KROWS) {
+      const uint32_t a = half + at[i] + kk * (32 * HR * 2);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(a));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(a + 4 * HR * 2));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *lds_ptr<const bf16x8>(half + at[kk] + i * 2048);
+    }
+  }
+};
+
+// Blocks are dispatched round-robin over the 8 XCDs: give each XCD a run of
+// consecutive tiles, and number the tiles in bands of 4 row tiles, column by
+// column, so that the tiles an XCD works on at once (about 4 x 8) share their
+// operand rows in its L2.
+__device__ __forceinline__ void tile_of_block(uint32_t b, uint32_t n, int32_t tiles_m, int32_t tiles_n, int32_t& tm,
+                                              int32_t& tn) {
+  const uint32_t x = b % kXcds, q = n / kXcds, r = n % kXcds;
+  const uint32_t t = x * q + min(x, r) + b / kXcds;
+  constexpr uint32_t kBand = 4;
+  const uint32_t band = t / (kBand * tiles_n), in = t % (kBand * tiles_n);
+  const uint32_t rows = min(kBand, tiles_m - band * kBand);
+  tm = static_cast<int32_t>(band * kBand + in % rows);
+  tn = static_cast<int32_t>(in / rows);
+}
+
+// HM, HN: rows of a half of A and of B; WM x WN waves.  kGated: half 0 of B
+// holds gate rows, half 1 the same up rows, so a lane has both sums of its
+// columns.
+template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
+__global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
+  constexpr bool kGated = EPI == DenseEpi::kGated;
+  constexpr int NW = WM * WN;
+  constexpr int TM = HM / WM / 16, TN = HN / WN / 16;
+  using SA = Source<HM, AT, NW>;
+  using SB = Source<HN, BT, NW>;
+  constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
+  constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes, kStage = 2 * (AB + BB);
+  // Two waves per SIMD and one block per CU: the waves of the upper row half
+  // run one step behind, so that on every SIMD one wave multiplies while the
+  // other reads LDS.
+  constexpr bool kPingPong = NW == 8;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[2 * kStage];
+
+  const DenseGemm& p = t.p;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t per_split = static_cast<uint32_t>(t.tiles_m) * t.tiles_n;
+  const int32_t split = blockIdx.x / per_split;
+  int32_t tm, tn;
+  tile_of_block(blockIdx.x % per_split, per_split, t.tiles_m, t.tiles_n, tm, tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * 2 * HM;
+  const int64_t n0 = static_cast<int64_t>(tn) * (kGated ? HN : 2 * HN);
+  const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * split / t.splits);
+  const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * (split + 1) / t.splits);
+  const int64_t k0 = static_cast<int64_t>(c0) * kChunk;
+  const int64_t ka = min(t.a_k, static_cast<int64_t>(c1) * kChunk), kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
+
+  SA a0(p.a, m0, t.a_r, k0, ka), a1(p.a, m0 + HM, t.a_r, k0, ka);
+  // kGated: the up rows are rows N + n of b
+  Operand up = p.b;
+  if constexpr (kGated) up.p += p.N * (BT ? 1 : p.b.ld);
+  SB b0(p.b, n0, t.b_r, k0, kb), b1(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb);
+  uint32_t va0[LA], va1[LA], vb0[LB], vb1[LB];
+  SA::lane_offsets(va0, a0.ld2, t.a_r - m0, wave, lane);
+  SA::lane_offsets(va1, a1.ld2, t.a_r - m0 - HM, wave, lane);
+  SB::lane_offsets(vb0, b0.ld2, t.b_r - n0, wave, lane);
+  SB::lane_offsets(vb1, b1.ld2, t.b_r - n0 - (kGated ? 0 : HN), wave, lane);
+  const int lane_k = 8 * ((lane & 7) ^ (lane >> 3));   // row operand: the k of the lane's copies
+  const Reader<HM, AT, TM> ra(wm * (HM / WM), lane);
+  const Reader<HN, BT, TN> rb(wn * (HN / WN), lane);
+
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_mem));
+  // places of the halves in a stage
+  constexpr uint32_t kA0 = 0, kA1 = AB, kB0 = 2 * AB, kB1 = 2 * AB + BB;
+
+  f32x4 acc[2][2][TM][TN];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  bf16x8 fa[TM][2], fb[2][TN][2];
+
+  a0.copy(va0, lane_k, lds + kA0, wave);
+  b0.copy(vb0, lane_k, lds + kB0, wave);
+  b1.copy(vb1, lane_k, lds + kB1, wave);
+  a1.copy(va1, lane_k, lds + kA1, wave);
+  a0.copy(va0, lane_k, lds + kStage + kA0, wave);
+  b0.copy(vb0, lane_k, lds + kStage + kB0, wave);
+  b1.copy(vb1, lane_k, lds + kStage + kB1, wave);
+  wait_copies<3 * LB + 2 * LA>();   // this wave's part of A0 and B0 of the first chunk
+  block_barrier();
+  if (kPingPong && wm == 1) block_barrier();
+
+#define DSMOE_READ_A(half)                                        \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = ra.read(st + (half), i, kk)
+#define DSMOE_READ_B(h, half)                                     \
+  _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[h][j][kk] = rb.read(st + (half), j, kk)
+  // The end of a phase's reads: they are done (the half may be refilled once
+  // all waves are past the barrier), and at most N younger copies of this wave
+  // are still on the way; then the phase's products.
+#define DSMOE_PHASE(ha, hb, wait)                                                                              \
+  do {                                                                                                         \
+    wait;                                                                                                      \
+    wait_lds();                                                                                                \
+    block_barrier();                                                                                           \
+    __builtin_amdgcn_sched_barrier(0);                                                                         \
+    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(1);                                                    \
+    _Pragma("unroll") for (int kk = 0; kk < 2; ++kk)                                                           \
+        _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                         \
+            _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[ha][hb][i][j] =                                 \
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[hb][j][kk], fa[i][kk], acc[ha][hb][i][j], 0, 0, 0); \
+    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(0);                                                    \
+    __builtin_amdgcn_sched_barrier(0);                                                                         \
+    if constexpr (kPingPong) block_barrier();                                                                  \
+  } while (0)
+
+  uint32_t st = lds, other = lds + kStage;
+  for (int32_t c = c0; c < c1; ++c) {
+    // phase 0: reads A0, B0; A1 of the next chunk goes out (its place was read
+    // in phase 2 of the previous chunk)
+    a1.copy(va1, lane_k, other + kA1, wave);
+    DSMOE_READ_A(kA0);
+    DSMOE_READ_B(0, kB0);
+    DSMOE_PHASE(0, 0, (wait_copies<3 * LA + 2 * LB>()));   // B1 is there
+    // phase 1
+    a0.copy(va0, lane_k, st + kA0, wave);
+    DSMOE_READ_B(1, kB1);
+    DSMOE_PHASE(0, 1, (wait_copies<3 * LA + 2 * LB>()));   // A1 is there
+    // phase 2
+    b0.copy(vb0, lane_k, st + kB0, wave);
+    DSMOE_READ_A(kA1);
+    DSMOE_PHASE(1, 1, (void)0);
+    // phase 3
+    b1.copy(vb1, lane_k, st + kB1, wave);
+    DSMOE_PHASE(1, 0, (wait_copies<3 * LB + 2 * LA>()));   // A0 and B0 of the next chunk are there
+    const uint32_t sw = st;
+    st = other;
+    other = sw;
+  }
+  if (kPingPong && wm == 0) block_barrier();
+#undef DSMOE_READ_A
+#undef DSMOE_READ_B
+#undef DSMOE_PHASE
+  wait_copies<0>();   // copies past the last chunk (zeros) land before the block ends
+
+  // A result lane holds row l % 16 of its A fragment and columns 4 (l / 16) +
+  // [0, 4) of its B fragment.  Where two B fragments are adjacent, swapping
+  // between neighbouring groups of 16 lanes leaves each lane 8 adjacent
+  // columns: 16 (g % 2) + 8 (g / 2) of the pair for lane group g.
+  constexpr int W = TN % 2 == 0 ? 8 : 4;
+  const int g = lane >> 4;
+  const int wcol = wn * (HN / WN) + (W == 8 ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g);
+  constexpr int NJ = TN / (W / 4);   // column runs of a lane per half
+  auto columns = [&](int ha, int hb, int i, int j, float* v) {
+    if constexpr (W == 8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[ha][hb][i][2 * j][r]),
+                                                        __float_as_uint(acc[ha][hb][i][2 * j + 1][r]), false, false);
+        v[r] = __uint_as_float(s[0]);
+        v[4 + r] = __uint_as_float(s[1]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = acc[ha][hb][i][j][r];
+    }
+  };
+  const int64_t row0 = m0 + wm * (HM / WM) + (lane & 15);
+  if (t.splits > 1) {
+    const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t n = n0 + wcol + j * 4 * W + (kGated ? 0 : hb * HN);
+        const int64_t pn = kGated ? n + hb * half_n : n;
+#pragma unroll
+        for (int hi = 0; hi < 2 * TM; ++hi) {
+          const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
+          float v[W];
+          columns(hi / TM, hb, hi % TM, j, v);
+          if (m < p.M && n < half_n)
+            store_cols<W>(t.partial, (split * p.M + m) * t.ldp + pn, true, true, W, v);
+        }
+      }
+    return;
+  }
+  if constexpr (kGated) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t n = n0 + wcol + j * 4 * W;
+#pragma unroll
+      for (int hi = 0; hi < 2 * TM; ++hi) {
+        const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
+        float gv[W], uv[W];
+        columns(hi / TM, 0, hi % TM, j, gv);
+        columns(hi / TM, 1, hi % TM, j, uv);
+        if (m < p.M && n < p.N) finish_gated<W>(p, t.vec, m, n, gv, uv);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t n = n0 + hb * HN + wcol + j * 4 * W;
+        float bias[W];
+        load_bias<W>(p, n, bias);
+#pragma unroll
+        for (int hi = 0; hi < 2 * TM; ++hi) {
+          const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
+          float v[W];
+          columns(hi / TM, hb, hi % TM, j, v);
+          if (m < p.M && n < p.N) finish_linear<W>(p, t.vec, m, n, v, bias);
+        }
+      }
+  }
+}
+
+// Sum of the splits' partial results in order, then the epilogue: 8 columns
+// of a row per thread.
+template <DenseEpi EPI>
+__global__ __launch_bounds__(256) void join_splits_kernel(TileArgs t) {
+  const DenseGemm& p = t.p;
+  const int64_t runs = (p.N + 7) / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.M * runs) return;
+  const int64_t m = i / runs, n = i % runs * 8;
+  auto sum = [&](int64_t at, float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    const float* q = t.partial + m * t.ldp + at;
+    for (int s = 0; s < t.splits; ++s, q += p.M * t.ldp) {
+      float o[8];
+      load_cols<8>(q, 0, true, true, 8, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += o[e];
+    }
+  };
+  float v[8];
+  sum(n, v);
+  if constexpr (EPI == DenseEpi::kGated) {
+    float u[8];
+    sum(runs * 8 + n, u);
+    finish_gated<8>(p, t.vec, m, n, v, u);
+  } else {
+    float bias[8];
+    load_bias<8>(p, n, bias);
+    finish_linear<8>(p, t.vec, m, n, v, bias);
+  }
+}
+
+// dst [rows][ldd] = src [rows][cols], the row's padding up to ldd zeroed.
+__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t* __restrict__ src, int64_t lds, int64_t rows,
+                                                        int64_t cols, uint16_t* __restrict__ dst, int64_t ldd) {
+  const int64_t segs = ldd / 8, n = rows * segs;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / segs, c = i % segs * 8;
+    const uint16_t* q = src + r * lds + c;
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? q[e] : 0;
+    *reinterpret_cast<u32x4*>(dst + r * ldd + c) =
+        u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
   }
 }
 
 __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd, bool f32, int64_t m, int64_t n) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < m * n;
-       i += static_cast<int64_t>(gridDim.x) * 256)
-    store1(dst, i / n * ldd + i % n, f32, 0.0f);
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t at = i / n * ldd + i % n;
+    if (f32)
+      static_cast<float*>(dst)[at] = 0.0f;
+    else
+      static_cast<uint16_t*>(dst)[at] = 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+enum class Shape { k256x256, k128x128, k64x128 };
+struct Plan {
+  Shape shape;
+  int splits;
+  int64_t tiles_m, tiles_n, chunks;
+  bool pack_a, pack_b;
+  int64_t a_rows, a_cols, b_rows, b_cols;   // of the stored matrices
+  size_t a_bytes, b_bytes, partial_bytes;
+};
+
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// whether the tile kernel can copy an operand whose rows hold `cols` values
+bool copyable(const Operand& o, int64_t cols) {
+  return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.ld % 8 == 0 && (cols % 8 == 0 || o.padded);
+}
+
+void shape_size(Shape s, int64_t& bm, int64_t& bn) {
+  bm = s == Shape::k256x256 ? 256 : s == Shape::k128x128 ? 128 : 64;
+  bn = s == Shape::k256x256 ? 256 : 128;
+}
+
+Plan make_plan(const DenseGemm& p) {
+  Plan pl{};
+  const bool gated = p.epi == DenseEpi::kGated;
+  const int64_t nb = gated ? 2 * p.N : p.N;   // rows of b
+  pl.a_rows = p.a.k_rows ? p.K : p.M, pl.a_cols = p.a.k_rows ? p.M : p.K;
+  pl.b_rows = p.b.k_rows ? p.K : nb, pl.b_cols = p.b.k_rows ? nb : p.K;
+  pl.pack_a = !copyable(p.a, pl.a_cols);
+  pl.pack_b = !copyable(p.b, pl.b_cols);
+  pl.a_bytes = pl.pack_a ? up256(static_cast<size_t>(pl.a_rows) * up8(pl.a_cols) * 2) : 0;
+  pl.b_bytes = pl.pack_b ? up256(static_cast<size_t>(pl.b_rows) * up8(pl.b_cols) * 2) : 0;
+  pl.chunks = (p.K + kChunk - 1) / kChunk;
+
+  // Shape and number of splits of K by the estimated time: rounds of blocks
+  // times a block's chunks, plus the partial sums' way through memory.
+  double best = 1e30;
+  for (Shape s : {Shape::k256x256, Shape::k128x128, Shape::k64x128}) {
+    int64_t bm, bn;
+    shape_size(s, bm, bn);
+    const int64_t tm = (p.M + bm - 1) / bm, tn = (nb + bn - 1) / bn;
+    // us per chunk of one block with the CU full, blocks per CU
+    const double chunk_us = s == Shape::k256x256 ? 1.45 : s == Shape::k128x128 ? 1.0 : 1.2;
+    const int64_t slots = 256 * (s == Shape::k256x256 ? 1 : s == Shape::k128x128 ? 2 : 3);
+    for (int sp = 1; sp <= 32 && sp <= pl.chunks; sp *= 2) {
+      const int64_t rounds = (tm * tn * sp + slots - 1) / slots;
+      double us = rounds * (static_cast<double>((pl.chunks + sp - 1) / sp) * chunk_us + 3.0);
+      if (sp > 1) us += 4.0 + 2.0 * sp * p.M * nb * 4 / 4e6;
+      if (us < best) {
+        best = us;
+        pl.shape = s, pl.splits = sp, pl.tiles_m = tm, pl.tiles_n = tn;
+      }
+    }
+  }
+  pl.partial_bytes = pl.splits > 1 ? static_cast<size_t>(pl.splits) * p.M * (gated ? 2 * up8(p.N) : up8(p.N)) * 4 : 0;
+  return pl;
+}
+
+hipError_t pack(const Operand& o, int64_t rows, int64_t cols, uint16_t* dst, hipStream_t s) {
+  const int64_t n = rows * (up8(cols) / 8), blocks = (n + 255) / 256;
+  pack_rows_kernel<<<static_cast<uint32_t>(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(o.p, o.ld, rows, cols, dst,
+                                                                                     up8(cols));
+  return hipGetLastError();
+}
+
+template <int HM, int HN, int WM, int WN>
+hipError_t launch_shape(const TileArgs& t, hipStream_t s) {
+  const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(t.tiles_m) * t.tiles_n * t.splits);
+  constexpr int threads = 64 * WM * WN;
+  if (t.p.epi == DenseEpi::kGated)   // forward only: both operands by rows
+    dense_tile_kernel<HM, HN, WM, WN, false, false, DenseEpi::kGated><<<grid, threads, 0, s>>>(t);
+  else if (!t.p.b.k_rows)
+    dense_tile_kernel<HM, HN, WM, WN, false, false, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
+  else if (!t.p.a.k_rows)
+    dense_tile_kernel<HM, HN, WM, WN, false, true, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
+  else
+    dense_tile_kernel<HM, HN, WM, WN, true, true, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
+  return hipGetLastError();
+}
+
+bool row16(const void* p, int64_t ld, int es) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
 }
 
 }  // namespace
 
-size_t dense_gemm_workspace_bytes(const DenseGemm& p) { return 0; }
+bool operand_copyable(const Operand& o, int64_t cols) { return copyable(o, cols); }
+
+size_t dense_gemm_workspace_bytes(const DenseGemm& p) {
+  const Plan pl = make_plan(p);
+  return pl.a_bytes + pl.b_bytes + up256(pl.partial_bytes);
+}
 
 hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
-  const int bn = p.epi == DenseEpi::kGated ? 32 : 64;
-  const int64_t grid = (p.M + 63) / 64 * ((p.N + bn - 1) / bn);
-  if (p.epi == DenseEpi::kGated)
-    dense_gemm_kernel<DenseEpi::kGated><<<static_cast<uint32_t>(grid), 256, 0, s>>>(p);
+  const Plan pl = make_plan(p);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  TileArgs t{};
+  t.p = p;
+  hipError_t e = hipSuccess;
+  if (pl.pack_a) {
+    uint16_t* d = reinterpret_cast<uint16_t*>(ws);
+    if ((e = pack(p.a, pl.a_rows, pl.a_cols, d, s)) != hipSuccess) return e;
+    t.p.a = Operand{d, up8(pl.a_cols), p.a.k_rows, true};
+  }
+  if (pl.pack_b) {
+    uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.a_bytes);
+    if ((e = pack(p.b, pl.b_rows, pl.b_cols, d, s)) != hipSuccess) return e;
+    t.p.b = Operand{d, up8(pl.b_cols), p.b.k_rows, true};
+  }
+  const bool gated = p.epi == DenseEpi::kGated;
+  // padded rows read as zeros up to a multiple of 8
+  t.a_k = p.a.k_rows ? p.K : up8(p.K);
+  t.b_k = p.b.k_rows ? p.K : up8(p.K);
+  t.a_r = p.a.k_rows ? up8(p.M) : p.M;
+  t.b_r = p.b.k_rows ? up8(p.N) : p.N;
+  t.vec = row16(p.y, p.ldy, p.y_f32 ? 4 : 2) && row16(p.residual, p.ldr, p.y_f32 ? 4 : 2) &&
+          row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && (!gated || !p.z || p.N % 8 == 0);
+  t.splits = pl.splits;
+  t.chunks = static_cast<int32_t>(pl.chunks);
+  t.tiles_m = static_cast<int32_t>(pl.tiles_m);
+  t.tiles_n = static_cast<int32_t>(pl.tiles_n);
+  if (pl.splits > 1) {
+    t.partial = reinterpret_cast<float*>(ws + pl.a_bytes + pl.b_bytes);
+    t.ldp = gated ? 2 * up8(p.N) : up8(p.N);
+  }
+  switch (pl.shape) {
+    case Shape::k256x256: e = launch_shape<128, 128, 2, 4>(t, s); break;
+    case Shape::k128x128: e = launch_shape<64, 64, 2, 2>(t, s); break;
+    case Shape::k64x128: e = launch_shape<32, 64, 1, 4>(t, s); break;
+  }
+  if (e != hipSuccess || pl.splits == 1) return e;
+  const int64_t blocks = (p.M * (up8(p.N) / 8) + 255) / 256;
+  if (gated)
+    join_splits_kernel<DenseEpi::kGated><<<static_cast<uint32_t>(blocks), 256, 0, s>>>(t);
   else
-    dense_gemm_kernel<DenseEpi::kLinear><<<static_cast<uint32_t>(grid), 256, 0, s>>>(p);
+    join_splits_kernel<DenseEpi::kLinear><<<static_cast<uint32_t>(blocks), 256, 0, s>>>(t);
   return hipGetLastError();
 }
 
