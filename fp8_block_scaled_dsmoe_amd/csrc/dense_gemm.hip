@@ -7,13 +7,19 @@
 // One kernel, dense_tile_kernel, in several tile shapes.  A block computes a
 // BM x BN tile in steps of 64 of K ("chunks").  Both operand tiles are split
 // in two halves (rows [0, BM/2) and [BM/2, BM), and so for B), and every wave
-// owns an equal part of each half, so that a chunk falls into four phases,
-//     (A0 B0) (A0 B1) (A1 B1) (A1 B0),
-// each a quarter of the tile's multiply-adds that needs one new half (two in
-// the first) read from LDS into registers.  Once every wave has read a half,
-// its place in LDS is refilled with the same half of the chunk two ahead by
-// asynchronous copies (buffer loads straight to LDS), one half per phase: the
-// copies have six phases to arrive, and only two chunks are ever in LDS.
+// owns an equal part of each half, so that a chunk falls into two phases, A0
+// with both halves of B and A1 with both, each half of the tile's
+// multiply-adds.  Once every wave has read a half from LDS into registers, its
+// place is refilled with the same half of the chunk two ahead by asynchronous
+// copies (buffer loads straight to LDS); the copies have a whole chunk to
+// arrive, and only two chunks are ever in LDS.  In the 256 x 256 tile the two
+// waves of a SIMD run half a phase apart, one multiplying while the other
+// reads.  8192^3 takes 0.78 ms, 1.41 PFLOP/s: the multiplies alone keep the
+// matrix cores busy 75% of the cycles, and the card lowers its clock under
+// this load (to 1.8 GHz of 2.4), so LDS and memory traffic cost time through
+// power as well.  Four phases per chunk (A0 B0, A0 B1, A1 B1, A1 B0) took
+// 0.82 ms: twice the barriers, and reads crowded into two of the phases; four
+// waves of 128 x 128 with the reads between their own products 0.83 ms.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,70 +47,59 @@ constexpr int kChunk = 64;   // K per chunk
 constexpr int kXcds = 8;
 
 // ---------------------------------------------------------------------------
-// Epilogue: W (4 or 8) adjacent columns of one row.
+// Epilogue: 8 adjacent columns of one row.
 // ---------------------------------------------------------------------------
 
-// columns i .. i + W - 1 of a row at base (f32 or bf16); valid of them exist.
-// vec: i-th element 4 W (2 W) byte aligned and all W exist.
-template <int W>
-__device__ __forceinline__ void load_cols(const void* base, int64_t i, bool f32, bool vec, int valid, float* o) {
+// columns i .. i + 7 of a matrix at base (f32 or bf16), of which `valid`
+// exist; vec: all 8 do and the accesses are 16-byte aligned
+__device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, bool vec, int valid, float* o) {
   if (f32) {
     const float* q = static_cast<const float*>(base) + i;
     if (vec) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(q), b = *reinterpret_cast<const f32x4*>(q + 4);
 #pragma unroll
-      for (int j = 0; j < W; j += 4) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(q + j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j + e] = a[e];
-      }
+      for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
     } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e) o[e] = e < valid ? q[e] : 0.0f;
+      for (int e = 0; e < 8; ++e) o[e] = e < valid ? q[e] : 0.0f;
     }
   } else {
     const uint16_t* q = static_cast<const uint16_t*>(base) + i;
     if (vec) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(q);
 #pragma unroll
-      for (int j = 0; j < W; j += 4) {
-        const u32x2 a = *reinterpret_cast<const u32x2*>(q + j);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          o[j + 2 * e] = __uint_as_float(a[e] << 16);
-          o[j + 2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-        }
+      for (int e = 0; e < 4; ++e) {
+        o[2 * e] = __uint_as_float(a[e] << 16);
+        o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e) o[e] = e < valid ? bf16_to_f32(q[e]) : 0.0f;
+      for (int e = 0; e < 8; ++e) o[e] = e < valid ? bf16_to_f32(q[e]) : 0.0f;
     }
   }
 }
 
-template <int W>
-__device__ __forceinline__ void store_cols(void* base, int64_t i, bool f32, bool vec, int valid, const float* v) {
+__device__ __forceinline__ void store8(void* base, int64_t i, bool f32, bool vec, int valid, const float* v) {
   if (f32) {
     float* q = static_cast<float*>(base) + i;
     if (vec) {
-#pragma unroll
-      for (int j = 0; j < W; j += 4) *reinterpret_cast<f32x4*>(q + j) = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+      *reinterpret_cast<f32x4*>(q) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
     } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e)
+      for (int e = 0; e < 8; ++e)
         if (e < valid) q[e] = v[e];
     }
   } else {
     uint16_t* q = static_cast<uint16_t*>(base) + i;
     if (vec) {
-      uint32_t a[W / 2];
+      u32x4 a;
 #pragma unroll
-      for (int e = 0; e < W / 2; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-      if constexpr (W == 8)
-        *reinterpret_cast<u32x4*>(q) = u32x4{a[0], a[1], a[2], a[3]};
-      else
-        *reinterpret_cast<u32x2*>(q) = u32x2{a[0], a[1]};
+      for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+      *reinterpret_cast<u32x4*>(q) = a;
     } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e)
+      for (int e = 0; e < 8; ++e)
         if (e < valid) q[e] = static_cast<uint16_t>(f32x2_to_bf16x2(v[e], 0.0f));
     }
   }
@@ -123,47 +118,44 @@ struct TileArgs {
 };
 
 // y = act(acc + bias) + residual, z = acc + bias
-template <int W>
 __device__ __forceinline__ void finish_linear(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* v,
                                               const float* bias) {
-  const int valid = static_cast<int>(min(static_cast<int64_t>(W), p.N - n));
-  const bool vec = pvec && valid == W;
+  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
+  const bool vec = pvec && valid == 8;
 #pragma unroll
-  for (int e = 0; e < W; ++e) v[e] += bias[e];
-  if (p.z) store_cols<W>(p.z, m * p.ldz + n, p.y_f32, vec, valid, v);
+  for (int e = 0; e < 8; ++e) v[e] += bias[e];
+  if (p.z) store8(p.z, m * p.ldz + n, p.y_f32, vec, valid, v);
   if (p.act != DSMOE_ACT_NONE) {
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = act_f32(p.act, v[e]);
+    for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, v[e]);
   }
   if (p.residual) {
-    float r[W];
-    load_cols<W>(p.residual, m * p.ldr + n, p.y_f32, vec, valid, r);
+    float r[8];
+    load8(p.residual, m * p.ldr + n, p.y_f32, vec, valid, r);
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[e] += r[e];
+    for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  store_cols<W>(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+  store8(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
 }
 
 // a = act(g) u, h = [g | u]
-template <int W>
 __device__ __forceinline__ void finish_gated(const DenseGemm& p, bool pvec, int64_t m, int64_t n, const float* g,
                                              const float* u) {
-  const int valid = static_cast<int>(min(static_cast<int64_t>(W), p.N - n));
-  const bool vec = pvec && valid == W;
+  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
+  const bool vec = pvec && valid == 8;
   if (p.z) {
-    store_cols<W>(p.z, m * p.ldz + n, false, vec, valid, g);
-    store_cols<W>(p.z, m * p.ldz + p.N + n, false, vec, valid, u);
+    store8(p.z, m * p.ldz + n, false, vec, valid, g);
+    store8(p.z, m * p.ldz + p.N + n, false, vec, valid, u);
   }
-  float v[W];
+  float v[8];
 #pragma unroll
-  for (int e = 0; e < W; ++e) v[e] = act_f32(p.act, g[e]) * u[e];
-  store_cols<W>(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+  for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, g[e]) * u[e];
+  store8(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
 }
 
-template <int W>
 __device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* o) {
 #pragma unroll
-  for (int e = 0; e < W; ++e) {
+  for (int e = 0; e < 8; ++e) {
     o[e] = 0.0f;
     if (p.bias && n + e < p.N)
       o[e] = p.bias_f32 ? static_cast<const float*>(p.bias)[n + e]
@@ -258,20 +250,25 @@ struct Source {
     r.w = 0x00020000;
     return r;
   }
-  // Issue this wave's copies of the current chunk to the half at lds, move on.
-  // voff: the lane's offsets (lane_offsets); lane_k: the first k of its
-  // segment (row operand).
-  __device__ __forceinline__ void copy(const uint32_t (&voff)[H::kCopies], int lane_k, uint32_t lds, int wave) {
-    const i32x4 rs = resource();
-#pragma unroll
-    for (int i = 0; i < H::kCopies; ++i) {
-      // a segment past the row's last valid k would read the next row
-      const uint32_t v = KROWS || lane_k < k_left ? voff[i] : 0x80000000u;
-      copy16(rs, v, __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
-    }
+  // Issue this wave's i-th copy of the current chunk to the half at lds.
+  // rs: resource(); voff: the lane's offsets (lane_offsets); lane_k: the first
+  // k of its segment (row operand).
+  __device__ __forceinline__ void copy(const i32x4& rs, int i, const uint32_t (&voff)[H::kCopies], int lane_k,
+                                       uint32_t lds, int wave) const {
+    // a segment past the row's last valid k would read the next row
+    const uint32_t v = KROWS || lane_k < k_left ? voff[i] : 0x80000000u;
+    copy16(rs, v, __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
+  }
+  __device__ __forceinline__ void advance() {
     base += step;
     if constexpr (!KROWS) range -= 2 * kChunk;
     k_left -= kChunk;
+  }
+  __device__ __forceinline__ void copy_all(const uint32_t (&voff)[H::kCopies], int lane_k, uint32_t lds, int wave) {
+    const i32x4 rs = resource();
+#pragma unroll
+    for (int i = 0; i < H::kCopies; ++i) copy(rs, i, voff, lane_k, lds, wave);
+    advance();
   }
   // The lane's byte offsets from base; cols_left: valid columns (k-row operand).
   static __device__ __forceinline__ void lane_offsets(uint32_t (&voff)[H::kCopies], uint32_t ld2, int64_t cols_left,
@@ -348,11 +345,13 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
   using SB = Source<HN, BT, NW>;
   constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
   constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes, kStage = 2 * (AB + BB);
+  constexpr int kOutStride = 2 * HN + 4;   // floats between rows of results in LDS
+  constexpr int kLds = 2 * kStage > HM * kOutStride * 4 ? 2 * kStage : HM * kOutStride * 4;
   // Two waves per SIMD and one block per CU: the waves of the upper row half
-  // run one step behind, so that on every SIMD one wave multiplies while the
-  // other reads LDS.
+  // run half a phase behind, so that on every SIMD one wave multiplies while
+  // the other reads LDS.
   constexpr bool kPingPong = NW == 8;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[2 * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kLds];
 
   const DenseGemm& p = t.p;
   const int lane = threadIdx.x & 63;
@@ -394,66 +393,73 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  bf16x8 fa[TM][2], fb[2][TN][2];
+  bf16x8 fa[TM][2], fb[3][TN][2];
 
-  a0.copy(va0, lane_k, lds + kA0, wave);
-  b0.copy(vb0, lane_k, lds + kB0, wave);
-  b1.copy(vb1, lane_k, lds + kB1, wave);
-  a1.copy(va1, lane_k, lds + kA1, wave);
-  a0.copy(va0, lane_k, lds + kStage + kA0, wave);
-  b0.copy(vb0, lane_k, lds + kStage + kB0, wave);
-  b1.copy(vb1, lane_k, lds + kStage + kB1, wave);
-  wait_copies<3 * LB + 2 * LA>();   // this wave's part of A0 and B0 of the first chunk
+  const uint32_t s0 = lds, s1 = lds + kStage;
+  b0.copy_all(vb0, lane_k, s0 + kB0, wave);
+  a0.copy_all(va0, lane_k, s0 + kA0, wave);
+  b1.copy_all(vb1, lane_k, s0 + kB1, wave);
+  a1.copy_all(va1, lane_k, s0 + kA1, wave);
+  b0.copy_all(vb0, lane_k, s1 + kB0, wave);
+  a0.copy_all(va0, lane_k, s1 + kA0, wave);
+  b1.copy_all(vb1, lane_k, s1 + kB1, wave);
+  wait_copies<2 * LA + 2 * LB>();   // this wave's part of B0, A0 and B1 of the first chunk
+  block_barrier();
+#define DSMOE_READ_A(from)                                        \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = ra.read(from, i, kk)
+#define DSMOE_READ_B(f, from)                                     \
+  _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = rb.read(from, j, kk)
+  // The end of a phase's reads and copies: the reads are done (the halves may
+  // be refilled once all waves are past the barrier), and what the next phase
+  // reads is there (at most the copies of this phase and the last may still be
+  // on the way).  Then the phase's products: both halves of B with A's half
+  // ha, B0 in fb[0], B1 in fb[1].
+#define DSMOE_PHASE(ha)                                                                                          \
+  do {                                                                                                           \
+    wait_copies<2 * LA + 2 * LB>();                                                                              \
+    wait_lds();                                                                                                  \
+    block_barrier();                                                                                             \
+    __builtin_amdgcn_sched_barrier(0);                                                                           \
+    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(1);                                                      \
+    _Pragma("unroll") for (int kk = 0; kk < 2; ++kk)                                                             \
+        _Pragma("unroll") for (int hb = 0; hb < 2; ++hb)                                                         \
+            _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                       \
+                _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[ha][hb][i][j] =                               \
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[hb][j][kk], fa[i][kk], acc[ha][hb][i][j], 0, 0, 0); \
+    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(0);                                                      \
+    __builtin_amdgcn_sched_barrier(0);                                                                           \
+    if constexpr (kPingPong) block_barrier();                                                                    \
+  } while (0)
+  DSMOE_READ_B(0, s0 + kB0);
+  wait_lds();
   block_barrier();
   if (kPingPong && wm == 1) block_barrier();
 
-#define DSMOE_READ_A(half)                                        \
-  _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = ra.read(st + (half), i, kk)
-#define DSMOE_READ_B(h, half)                                     \
-  _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[h][j][kk] = rb.read(st + (half), j, kk)
-  // The end of a phase's reads: they are done (the half may be refilled once
-  // all waves are past the barrier), and at most N younger copies of this wave
-  // are still on the way; then the phase's products.
-#define DSMOE_PHASE(ha, hb, wait)                                                                              \
-  do {                                                                                                         \
-    wait;                                                                                                      \
-    wait_lds();                                                                                                \
-    block_barrier();                                                                                           \
-    __builtin_amdgcn_sched_barrier(0);                                                                         \
-    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(1);                                                    \
-    _Pragma("unroll") for (int kk = 0; kk < 2; ++kk)                                                           \
-        _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                         \
-            _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[ha][hb][i][j] =                                 \
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[hb][j][kk], fa[i][kk], acc[ha][hb][i][j], 0, 0, 0); \
-    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(0);                                                    \
-    __builtin_amdgcn_sched_barrier(0);                                                                         \
-    if constexpr (kPingPong) block_barrier();                                                                  \
-  } while (0)
-
-  uint32_t st = lds, other = lds + kStage;
+  // The next chunk's B0 is read in the second phase, to even out the phases'
+  // reads; it has registers of its own and moves at the end.
+  uint32_t st = s0, nx = s1;
   for (int32_t c = c0; c < c1; ++c) {
-    // phase 0: reads A0, B0; A1 of the next chunk goes out (its place was read
-    // in phase 2 of the previous chunk)
-    a1.copy(va1, lane_k, other + kA1, wave);
-    DSMOE_READ_A(kA0);
-    DSMOE_READ_B(0, kB0);
-    DSMOE_PHASE(0, 0, (wait_copies<3 * LA + 2 * LB>()));   // B1 is there
-    // phase 1
-    a0.copy(va0, lane_k, st + kA0, wave);
-    DSMOE_READ_B(1, kB1);
-    DSMOE_PHASE(0, 1, (wait_copies<3 * LA + 2 * LB>()));   // A1 is there
-    // phase 2
-    b0.copy(vb0, lane_k, st + kB0, wave);
-    DSMOE_READ_A(kA1);
-    DSMOE_PHASE(1, 1, (void)0);
-    // phase 3
-    b1.copy(vb1, lane_k, st + kB1, wave);
-    DSMOE_PHASE(1, 0, (wait_copies<3 * LB + 2 * LA>()));   // A0 and B0 of the next chunk are there
+    DSMOE_READ_A(st + kA0);
+    DSMOE_READ_B(1, st + kB1);
+    __builtin_amdgcn_sched_barrier(0);
+    a1.copy_all(va1, lane_k, nx + kA1, wave);
+    b0.copy_all(vb0, lane_k, st + kB0, wave);
+    DSMOE_PHASE(0);
+    DSMOE_READ_A(st + kA1);
+    DSMOE_READ_B(2, nx + kB0);
+    __builtin_amdgcn_sched_barrier(0);
+    a0.copy_all(va0, lane_k, st + kA0, wave);
+    b1.copy_all(vb1, lane_k, st + kB1, wave);
+    DSMOE_PHASE(1);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) fb[0][j][kk] = fb[2][j][kk];
     const uint32_t sw = st;
-    st = other;
-    other = sw;
+    st = nx;
+    nx = sw;
   }
   if (kPingPong && wm == 0) block_barrier();
 #undef DSMOE_READ_A
@@ -461,77 +467,57 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
 #undef DSMOE_PHASE
   wait_copies<0>();   // copies past the last chunk (zeros) land before the block ends
 
-  // A result lane holds row l % 16 of its A fragment and columns 4 (l / 16) +
-  // [0, 4) of its B fragment.  Where two B fragments are adjacent, swapping
-  // between neighbouring groups of 16 lanes leaves each lane 8 adjacent
-  // columns: 16 (g % 2) + 8 (g / 2) of the pair for lane group g.
-  constexpr int W = TN % 2 == 0 ? 8 : 4;
-  const int g = lane >> 4;
-  const int wcol = wn * (HN / WN) + (W == 8 ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g);
-  constexpr int NJ = TN / (W / 4);   // column runs of a lane per half
-  auto columns = [&](int ha, int hb, int i, int j, float* v) {
-    if constexpr (W == 8) {
+  // The results pass through LDS, half of the tile's rows at a time, so that a
+  // thread finishes runs of 8 columns and a wave writes whole lines.  A result
+  // lane holds row l % 16 of its A fragment and columns 4 (l / 16) + [0, 4) of
+  // its B fragment; rows 16 bytes off a multiple of 256 apart keep the writes
+  // of 16 rows on separate banks.
+  constexpr int kRuns = (kGated ? HN : 2 * HN) / 8, kRowsAtOnce = 64 * NW / kRuns;
+  static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
+  const int run = threadIdx.x % kRuns;
+  const int64_t n = n0 + run * 8;
+  const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
+  float bias[8] = {};
+  if (!kGated && t.splits == 1) load_bias(p, n, bias);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[ha][hb][i][2 * j][r]),
-                                                        __float_as_uint(acc[ha][hb][i][2 * j + 1][r]), false, false);
-        v[r] = __uint_as_float(s[0]);
-        v[4 + r] = __uint_as_float(s[1]);
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = acc[ha][hb][i][j][r];
-    }
-  };
-  const int64_t row0 = m0 + wm * (HM / WM) + (lane & 15);
-  if (t.splits > 1) {
-    const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
+  for (int ha = 0; ha < 2; ++ha) {
+    block_barrier();   // LDS is free (the last reads were waited for)
 #pragma unroll
     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t n = n0 + wcol + j * 4 * W + (kGated ? 0 : hb * HN);
-        const int64_t pn = kGated ? n + hb * half_n : n;
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int hi = 0; hi < 2 * TM; ++hi) {
-          const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
-          float v[W];
-          columns(hi / TM, hb, hi % TM, j, v);
-          if (m < p.M && n < half_n)
-            store_cols<W>(t.partial, (split * p.M + m) * t.ldp + pn, true, true, W, v);
+        for (int j = 0; j < TN; ++j) {
+          const int r = wm * (HM / WM) + 16 * i + (lane & 15);
+          const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
+          *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[ha][hb][i][j];
         }
+    wait_lds();
+    block_barrier();
+#pragma unroll 1
+    for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
+      const int64_t m = m0 + ha * HM + r;
+      if (m >= p.M || n >= half_n) break;
+      const uint32_t at = lds + (r * kOutStride + run * 8) * 4;
+      float v[8], u[8];
+      const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
+      if constexpr (kGated) {
+        const f32x4 u0 = *lds_ptr<const f32x4>(at + HN * 4), u1 = *lds_ptr<const f32x4>(at + HN * 4 + 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = u0[e], u[4 + e] = u1[e];
       }
-    return;
-  }
-  if constexpr (kGated) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t n = n0 + wcol + j * 4 * W;
-#pragma unroll
-      for (int hi = 0; hi < 2 * TM; ++hi) {
-        const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
-        float gv[W], uv[W];
-        columns(hi / TM, 0, hi % TM, j, gv);
-        columns(hi / TM, 1, hi % TM, j, uv);
-        if (m < p.M && n < p.N) finish_gated<W>(p, t.vec, m, n, gv, uv);
+      if (t.splits > 1) {
+        store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
+        if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
+      } else if constexpr (kGated) {
+        finish_gated(p, t.vec, m, n, v, u);
+      } else {
+        finish_linear(p, t.vec, m, n, v, bias);
       }
     }
-  } else {
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t n = n0 + hb * HN + wcol + j * 4 * W;
-        float bias[W];
-        load_bias<W>(p, n, bias);
-#pragma unroll
-        for (int hi = 0; hi < 2 * TM; ++hi) {
-          const int64_t m = row0 + (hi / TM) * HM + (hi % TM) * 16;
-          float v[W];
-          columns(hi / TM, hb, hi % TM, j, v);
-          if (m < p.M && n < p.N) finish_linear<W>(p, t.vec, m, n, v, bias);
-        }
-      }
+    wait_lds();
   }
 }
 
@@ -550,7 +536,7 @@ __global__ __launch_bounds__(256) void join_splits_kernel(TileArgs t) {
     const float* q = t.partial + m * t.ldp + at;
     for (int s = 0; s < t.splits; ++s, q += p.M * t.ldp) {
       float o[8];
-      load_cols<8>(q, 0, true, true, 8, o);
+      load8(q, 0, true, true, 8, o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += o[e];
     }
@@ -560,11 +546,11 @@ __global__ __launch_bounds__(256) void join_splits_kernel(TileArgs t) {
   if constexpr (EPI == DenseEpi::kGated) {
     float u[8];
     sum(runs * 8 + n, u);
-    finish_gated<8>(p, t.vec, m, n, v, u);
+    finish_gated(p, t.vec, m, n, v, u);
   } else {
     float bias[8];
-    load_bias<8>(p, n, bias);
-    finish_linear<8>(p, t.vec, m, n, v, bias);
+    load_bias(p, n, bias);
+    finish_linear(p, t.vec, m, n, v, bias);
   }
 }
 
