@@ -117,9 +117,14 @@ struct TileArgs {
   int32_t tiles_m, tiles_n;
 };
 
-// y = act(acc + bias) + residual, z = acc + bias
+__device__ __forceinline__ void load_residual(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* r) {
+  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
+  load8(p.residual, m * p.ldr + n, p.y_f32, pvec && valid == 8, valid, r);
+}
+
+// y = act(acc + bias) + residual (r, when has_res), z = acc + bias
 __device__ __forceinline__ void finish_linear(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* v,
-                                              const float* bias) {
+                                              const float* bias, bool has_res, const float (&r)[8]) {
   const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
   const bool vec = pvec && valid == 8;
 #pragma unroll
@@ -129,9 +134,7 @@ __device__ __forceinline__ void finish_linear(const DenseGemm& p, bool pvec, int
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, v[e]);
   }
-  if (p.residual) {
-    float r[8];
-    load8(p.residual, m * p.ldr + n, p.y_f32, vec, valid, r);
+  if (has_res) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
@@ -219,6 +222,7 @@ struct Source {
   uint32_t ld2;           // row stride in bytes
   int32_t k_left;         // valid k from base on
 
+  __device__ __forceinline__ Source() {}
   // rows [r0, r0 + HR) of the operand, chunks from k0 on, k_end: end of valid k
   __device__ __forceinline__ Source(const Operand& o, int64_t r0, int64_t rows, int64_t k0, int64_t k_end) {
     ld2 = static_cast<uint32_t>(o.ld * 2);
@@ -333,84 +337,192 @@ __device__ __forceinline__ void tile_of_block(uint32_t b, uint32_t n, int32_t ti
   tn = static_cast<int32_t>(in / rows);
 }
 
-// HM, HN: rows of a half of A and of B; WM x WN waves.  kGated: half 0 of B
-// holds gate rows, half 1 the same up rows, so a lane has both sums of its
-// columns.
+// What a block and its waves work on.  HM, HN: rows of a half of A and of B;
+// WM x WN waves.  kGated: half 0 of B holds gate rows, half 1 the same up
+// rows, so a lane has both sums of its columns.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
-__global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
-  constexpr bool kGated = EPI == DenseEpi::kGated;
-  constexpr int NW = WM * WN;
-  constexpr int TM = HM / WM / 16, TN = HN / WN / 16;
+struct Tile {
+  static constexpr bool kGated = EPI == DenseEpi::kGated;
+  static constexpr int NW = WM * WN;
+  static constexpr int TM = HM / WM / 16, TN = HN / WN / 16;   // fragments of a wave per half
   using SA = Source<HM, AT, NW>;
   using SB = Source<HN, BT, NW>;
-  constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
-  constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes, kStage = 2 * (AB + BB);
-  constexpr int kOutStride = 2 * HN + 4;   // floats between rows of results in LDS
-  constexpr int kLds = 2 * kStage > HM * kOutStride * 4 ? 2 * kStage : HM * kOutStride * 4;
-  // Two waves per SIMD and one block per CU: the waves of the upper row half
-  // run half a phase behind, so that on every SIMD one wave multiplies while
-  // the other reads LDS.
-  constexpr bool kPingPong = NW == 8;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kLds];
+  static constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
+  static constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes;
+  // a stage of LDS and the places of the halves in it
+  static constexpr uint32_t kStage = 2 * (AB + BB), kA0 = 0, kA1 = AB, kB0 = 2 * AB, kB1 = 2 * AB + BB;
+  static constexpr int kOutStride = 2 * HN + 4;   // floats between rows of results in LDS
+  static constexpr int lds_bytes(int stages) {
+    const int a = stages * kStage, b = HM * kOutStride * 4;
+    return a > b ? a : b;
+  }
+  typedef f32x4 Acc[2][2][TM][TN];   // [half of A][half of B]
 
-  const DenseGemm& p = t.p;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const uint32_t per_split = static_cast<uint32_t>(t.tiles_m) * t.tiles_n;
-  const int32_t split = blockIdx.x / per_split;
-  int32_t tm, tn;
-  tile_of_block(blockIdx.x % per_split, per_split, t.tiles_m, t.tiles_n, tm, tn);
-  const int64_t m0 = static_cast<int64_t>(tm) * 2 * HM;
-  const int64_t n0 = static_cast<int64_t>(tn) * (kGated ? HN : 2 * HN);
-  const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * split / t.splits);
-  const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * (split + 1) / t.splits);
-  const int64_t k0 = static_cast<int64_t>(c0) * kChunk;
-  const int64_t ka = min(t.a_k, static_cast<int64_t>(c1) * kChunk), kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
-
-  SA a0(p.a, m0, t.a_r, k0, ka), a1(p.a, m0 + HM, t.a_r, k0, ka);
-  // kGated: the up rows are rows N + n of b
-  Operand up = p.b;
-  if constexpr (kGated) up.p += p.N * (BT ? 1 : p.b.ld);
-  SB b0(p.b, n0, t.b_r, k0, kb), b1(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb);
+  const TileArgs& t;
+  const DenseGemm& p;
+  const int lane, wave, wm, wn;
+  int32_t split, c0, c1;   // split of K, its chunks
+  int64_t m0, n0;
+  SA a0, a1;
+  SB b0, b1;
   uint32_t va0[LA], va1[LA], vb0[LB], vb1[LB];
-  SA::lane_offsets(va0, a0.ld2, t.a_r - m0, wave, lane);
-  SA::lane_offsets(va1, a1.ld2, t.a_r - m0 - HM, wave, lane);
-  SB::lane_offsets(vb0, b0.ld2, t.b_r - n0, wave, lane);
-  SB::lane_offsets(vb1, b1.ld2, t.b_r - n0 - (kGated ? 0 : HN), wave, lane);
-  const int lane_k = 8 * ((lane & 7) ^ (lane >> 3));   // row operand: the k of the lane's copies
-  const Reader<HM, AT, TM> ra(wm * (HM / WM), lane);
-  const Reader<HN, BT, TN> rb(wn * (HN / WN), lane);
+  const int lane_k;        // row operand: the k of the lane's copies
+  const Reader<HM, AT, TM> ra;
+  const Reader<HN, BT, TN> rb;
+  const uint32_t lds;
 
-  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_mem));
-  // places of the halves in a stage
-  constexpr uint32_t kA0 = 0, kA1 = AB, kB0 = 2 * AB, kB1 = 2 * AB + BB;
+  __device__ __forceinline__ Tile(const TileArgs& args, const uint8_t* mem)
+      : t(args),
+        p(args.p),
+        lane(threadIdx.x & 63),
+        wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+        wm(wave / WN),
+        wn(wave % WN),
+        lane_k(8 * ((lane & 7) ^ (lane >> 3))),
+        ra(wm * (HM / WM), lane),
+        rb(wn * (HN / WN), lane),
+        lds(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(mem))) {
+    const uint32_t per_split = static_cast<uint32_t>(t.tiles_m) * t.tiles_n;
+    split = blockIdx.x / per_split;
+    int32_t tm, tn;
+    tile_of_block(blockIdx.x % per_split, per_split, t.tiles_m, t.tiles_n, tm, tn);
+    m0 = static_cast<int64_t>(tm) * 2 * HM;
+    n0 = static_cast<int64_t>(tn) * (kGated ? HN : 2 * HN);
+    c0 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * split / t.splits);
+    c1 = static_cast<int32_t>(static_cast<int64_t>(t.chunks) * (split + 1) / t.splits);
+    const int64_t k0 = static_cast<int64_t>(c0) * kChunk;
+    const int64_t ka = min(t.a_k, static_cast<int64_t>(c1) * kChunk);
+    const int64_t kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
+    a0 = SA(p.a, m0, t.a_r, k0, ka);
+    a1 = SA(p.a, m0 + HM, t.a_r, k0, ka);
+    Operand up = p.b;   // kGated: the up rows are rows N + n of b
+    if constexpr (kGated) up.p += p.N * (BT ? 1 : p.b.ld);
+    b0 = SB(p.b, n0, t.b_r, k0, kb);
+    b1 = SB(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb);
+    SA::lane_offsets(va0, a0.ld2, t.a_r - m0, wave, lane);
+    SA::lane_offsets(va1, a1.ld2, t.a_r - m0 - HM, wave, lane);
+    SB::lane_offsets(vb0, b0.ld2, t.b_r - n0, wave, lane);
+    SB::lane_offsets(vb1, b1.ld2, t.b_r - n0 - (kGated ? 0 : HN), wave, lane);
+  }
 
-  f32x4 acc[2][2][TM][TN];
+  // the wave's copies of the next chunk of a half into a stage
+  __device__ __forceinline__ void copy_a0(uint32_t stage) { a0.copy_all(va0, lane_k, stage + kA0, wave); }
+  __device__ __forceinline__ void copy_a1(uint32_t stage) { a1.copy_all(va1, lane_k, stage + kA1, wave); }
+  __device__ __forceinline__ void copy_b0(uint32_t stage) { b0.copy_all(vb0, lane_k, stage + kB0, wave); }
+  __device__ __forceinline__ void copy_b1(uint32_t stage) { b1.copy_all(vb1, lane_k, stage + kB1, wave); }
+
+  static __device__ __forceinline__ void clear(Acc& acc) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h)
+    for (int h = 0; h < 4; ++h)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  __device__ __forceinline__ void finish(const Acc& acc) const {
+    // The results pass through LDS, half of the tile's rows at a time, so that a
+    // thread finishes runs of 8 columns and a wave writes whole lines.  A result
+    // lane holds row l % 16 of its A fragment and columns 4 (l / 16) + [0, 4) of
+    // its B fragment; rows 16 bytes off a multiple of 256 apart keep the writes
+    // of 16 rows on separate banks.
+    constexpr int kRuns = (kGated ? HN : 2 * HN) / 8;   // of 8 columns
+    constexpr int kRowsAtOnce = 64 * NW / kRuns < HM ? 64 * NW / kRuns : HM;
+    static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
+    const int run = threadIdx.x % kRuns;
+    const int64_t n = n0 + run * 8;
+    const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
+    float bias[8] = {};
+    if (!kGated && t.splits == 1) load_bias(p, n, bias);
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha) {
+      block_barrier();   // LDS is free (the last reads were waited for)
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const int r = wm * (HM / WM) + 16 * i + (lane & 15);
+            const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
+            *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[ha][hb][i][j];
+          }
+      wait_lds();
+      block_barrier();
+      // kBatch rows at a time, their residuals loaded first: one row's residual
+      // at a time left each row waiting for memory in turn
+      constexpr int kBatch = HM / kRowsAtOnce % 4 == 0 ? 4 : HM / kRowsAtOnce % 2 == 0 ? 2 : 1;
+      const int64_t row0 = m0 + ha * HM;
+#pragma unroll 1
+      for (int r0 = threadIdx.x / kRuns; r0 < HM; r0 += kBatch * kRowsAtOnce) {
+        if (row0 + r0 >= p.M || n >= half_n) break;
+        float res[kBatch][8];
+        const bool has_res = !kGated && t.splits == 1 && p.residual && n < p.N;
+        if (has_res) {
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const int64_t m = row0 + r0 + q * kRowsAtOnce;
+            if (m < p.M) load_residual(p, t.vec, m, n, res[q]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int r = r0 + q * kRowsAtOnce;
+          const int64_t m = row0 + r;
+          if (m >= p.M) break;
+          const uint32_t at = lds + (r * kOutStride + run * 8) * 4;
+          float v[8], u[8];
+          const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
+          if constexpr (kGated) {
+            const f32x4 u0 = *lds_ptr<const f32x4>(at + HN * 4), u1 = *lds_ptr<const f32x4>(at + HN * 4 + 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = u0[e], u[4 + e] = u1[e];
+          }
+          if (t.splits > 1) {
+            store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
+            if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
+          } else if constexpr (kGated) {
+            finish_gated(p, t.vec, m, n, v, u);
+          } else if (n < p.N) {
+            finish_linear(p, t.vec, m, n, v, bias, has_res, res[q]);
+          }
+        }
+      }
+      wait_lds();
+    }
+  }
+};
+
+// The 256 x 256 tile: two stages of LDS refilled half by half.
+template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
+__global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs args) {
+  using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
+  constexpr int TM = T::TM, TN = T::TN, LA = T::LA, LB = T::LB;
+  static_assert(T::NW == 8, "two waves per SIMD");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(2)];
+  T w(args, s_mem);
+  typename T::Acc acc;
+  T::clear(acc);
   bf16x8 fa[TM][2], fb[3][TN][2];
 
-  const uint32_t s0 = lds, s1 = lds + kStage;
-  b0.copy_all(vb0, lane_k, s0 + kB0, wave);
-  a0.copy_all(va0, lane_k, s0 + kA0, wave);
-  b1.copy_all(vb1, lane_k, s0 + kB1, wave);
-  a1.copy_all(va1, lane_k, s0 + kA1, wave);
-  b0.copy_all(vb0, lane_k, s1 + kB0, wave);
-  a0.copy_all(va0, lane_k, s1 + kA0, wave);
-  b1.copy_all(vb1, lane_k, s1 + kB1, wave);
+  const uint32_t s0 = w.lds, s1 = w.lds + T::kStage;
+  w.copy_b0(s0);
+  w.copy_a0(s0);
+  w.copy_b1(s0);
+  w.copy_a1(s0);
+  w.copy_b0(s1);
+  w.copy_a0(s1);
+  w.copy_b1(s1);
   wait_copies<2 * LA + 2 * LB>();   // this wave's part of B0, A0 and B1 of the first chunk
   block_barrier();
 #define DSMOE_READ_A(from)                                        \
   _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = ra.read(from, i, kk)
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = w.ra.read(from, i, kk)
 #define DSMOE_READ_B(f, from)                                     \
   _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = rb.read(from, j, kk)
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = w.rb.read(from, j, kk)
   // The end of a phase's reads and copies: the reads are done (the halves may
   // be refilled once all waves are past the barrier), and what the next phase
   // reads is there (at most the copies of this phase and the last may still be
@@ -422,36 +534,36 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
     wait_lds();                                                                                                  \
     block_barrier();                                                                                             \
     __builtin_amdgcn_sched_barrier(0);                                                                           \
-    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(1);                                                      \
+    __builtin_amdgcn_s_setprio(1);                                                      \
     _Pragma("unroll") for (int kk = 0; kk < 2; ++kk)                                                             \
         _Pragma("unroll") for (int hb = 0; hb < 2; ++hb)                                                         \
             _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                       \
                 _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[ha][hb][i][j] =                               \
                     __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[hb][j][kk], fa[i][kk], acc[ha][hb][i][j], 0, 0, 0); \
-    if constexpr (kPingPong) __builtin_amdgcn_s_setprio(0);                                                      \
+    __builtin_amdgcn_s_setprio(0);                                                      \
     __builtin_amdgcn_sched_barrier(0);                                                                           \
-    if constexpr (kPingPong) block_barrier();                                                                    \
+    block_barrier();                                                                    \
   } while (0)
-  DSMOE_READ_B(0, s0 + kB0);
+  DSMOE_READ_B(0, s0 + T::kB0);
   wait_lds();
   block_barrier();
-  if (kPingPong && wm == 1) block_barrier();
+  if (w.wm == 1) block_barrier();
 
   // The next chunk's B0 is read in the second phase, to even out the phases'
   // reads; it has registers of its own and moves at the end.
   uint32_t st = s0, nx = s1;
-  for (int32_t c = c0; c < c1; ++c) {
-    DSMOE_READ_A(st + kA0);
-    DSMOE_READ_B(1, st + kB1);
+  for (int32_t c = w.c0; c < w.c1; ++c) {
+    DSMOE_READ_A(st + T::kA0);
+    DSMOE_READ_B(1, st + T::kB1);
     __builtin_amdgcn_sched_barrier(0);
-    a1.copy_all(va1, lane_k, nx + kA1, wave);
-    b0.copy_all(vb0, lane_k, st + kB0, wave);
+    w.copy_a1(nx);
+    w.copy_b0(st);
     DSMOE_PHASE(0);
-    DSMOE_READ_A(st + kA1);
-    DSMOE_READ_B(2, nx + kB0);
+    DSMOE_READ_A(st + T::kA1);
+    DSMOE_READ_B(2, nx + T::kB0);
     __builtin_amdgcn_sched_barrier(0);
-    a0.copy_all(va0, lane_k, st + kA0, wave);
-    b1.copy_all(vb1, lane_k, st + kB1, wave);
+    w.copy_a0(st);
+    w.copy_b1(st);
     DSMOE_PHASE(1);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
@@ -461,64 +573,69 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_tile_kernel(TileArgs t) {
     st = nx;
     nx = sw;
   }
-  if (kPingPong && wm == 0) block_barrier();
+  if (w.wm == 0) block_barrier();
 #undef DSMOE_READ_A
 #undef DSMOE_READ_B
 #undef DSMOE_PHASE
-  wait_copies<0>();   // copies past the last chunk (zeros) land before the block ends
+  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
+  w.finish(acc);
+}
 
-  // The results pass through LDS, half of the tile's rows at a time, so that a
-  // thread finishes runs of 8 columns and a wave writes whole lines.  A result
-  // lane holds row l % 16 of its A fragment and columns 4 (l / 16) + [0, 4) of
-  // its B fragment; rows 16 bytes off a multiple of 256 apart keep the writes
-  // of 16 rows on separate banks.
-  constexpr int kRuns = (kGated ? HN : 2 * HN) / 8, kRowsAtOnce = 64 * NW / kRuns;
-  static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
-  const int run = threadIdx.x % kRuns;
-  const int64_t n = n0 + run * 8;
-  const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
-  float bias[8] = {};
-  if (!kGated && t.splits == 1) load_bias(p, n, bias);
-#pragma unroll
-  for (int ha = 0; ha < 2; ++ha) {
-    block_barrier();   // LDS is free (the last reads were waited for)
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int r = wm * (HM / WM) + 16 * i + (lane & 15);
-          const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
-          *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[ha][hb][i][j];
-        }
+// Smaller tiles: S stages of LDS.  A chunk's fragments are read in two steps of
+// 32 of K, each while the products of the step before run; once a chunk's
+// second step is in registers in every wave, its stage is refilled with the
+// chunk S ahead.
+template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
+__global__ __launch_bounds__(64 * WM * WN) void dense_ring_kernel(TileArgs args) {
+  using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
+  constexpr int TM = T::TM, TN = T::TN, L = 2 * T::LA + 2 * T::LB;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(S)];
+  T w(args, s_mem);
+  typename T::Acc acc;
+  T::clear(acc);
+  bf16x8 fa[2][2][TM], fb[2][2][TN];   // [step][half]
+
+#define DSMOE_COPY(stage) w.copy_a0(stage), w.copy_b0(stage), w.copy_b1(stage), w.copy_a1(stage)
+#define DSMOE_READ(kk, stage)                                                                              \
+  do {                                                                                                     \
+    _Pragma("unroll") for (int h = 0; h < 2; ++h) {                                                        \
+      _Pragma("unroll") for (int i = 0; i < TM; ++i) fa[kk][h][i] =                                        \
+          w.ra.read((stage) + (h ? T::kA1 : T::kA0), i, kk);                                               \
+      _Pragma("unroll") for (int j = 0; j < TN; ++j) fb[kk][h][j] =                                        \
+          w.rb.read((stage) + (h ? T::kB1 : T::kB0), j, kk);                                               \
+    }                                                                                                      \
+  } while (0)
+#define DSMOE_PRODUCTS(kk)                                                                                 \
+  _Pragma("unroll") for (int h = 0; h < 4; ++h)                                                            \
+      _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                       \
+          _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] =                        \
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][h & 1][j], fa[kk][h >> 1][i],                 \
+                                                      acc[h >> 1][h & 1][i][j], 0, 0, 0)
+  for (int i = 0; i < S; ++i) DSMOE_COPY(w.lds + i * T::kStage);
+  wait_copies<(S - 1) * L>();
+  block_barrier();
+  uint32_t st = w.lds;
+  DSMOE_READ(0, st);
+  for (int32_t c = w.c0; c < w.c1; ++c) {
+    const uint32_t nx = st + T::kStage == w.lds + S * T::kStage ? w.lds : st + T::kStage;
+    DSMOE_READ(1, st);
+    DSMOE_PRODUCTS(0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_copies<(S - 2) * L>();   // the next chunk's copies of this wave
     wait_lds();
     block_barrier();
-#pragma unroll 1
-    for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
-      const int64_t m = m0 + ha * HM + r;
-      if (m >= p.M || n >= half_n) break;
-      const uint32_t at = lds + (r * kOutStride + run * 8) * 4;
-      float v[8], u[8];
-      const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
-      if constexpr (kGated) {
-        const f32x4 u0 = *lds_ptr<const f32x4>(at + HN * 4), u1 = *lds_ptr<const f32x4>(at + HN * 4 + 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = u0[e], u[4 + e] = u1[e];
-      }
-      if (t.splits > 1) {
-        store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
-        if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
-      } else if constexpr (kGated) {
-        finish_gated(p, t.vec, m, n, v, u);
-      } else {
-        finish_linear(p, t.vec, m, n, v, bias);
-      }
-    }
-    wait_lds();
+    DSMOE_COPY(st);
+    DSMOE_READ(0, nx);
+    DSMOE_PRODUCTS(1);
+    __builtin_amdgcn_sched_barrier(0);
+    st = nx;
   }
+#undef DSMOE_COPY
+#undef DSMOE_READ
+#undef DSMOE_PRODUCTS
+  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
+  wait_lds();
+  w.finish(acc);
 }
 
 // Sum of the splits' partial results in order, then the epilogue: 8 columns
@@ -550,7 +667,9 @@ __global__ __launch_bounds__(256) void join_splits_kernel(TileArgs t) {
   } else {
     float bias[8];
     load_bias(p, n, bias);
-    finish_linear(p, t.vec, m, n, v, bias);
+    float r[8];
+    if (p.residual) load_residual(p, t.vec, m, n, r);
+    finish_linear(p, t.vec, m, n, v, bias, p.residual != nullptr, r);
   }
 }
 
@@ -585,7 +704,28 @@ __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd
 // Host side
 // ---------------------------------------------------------------------------
 
-enum class Shape { k256x256, k128x128, k64x128 };
+// The tile shapes.  chunk_us: time of one chunk (64 of K) of one block, alone
+// on its CU and with a second block beside it; end_us: a block's start and
+// epilogue.  Measured on products of 2048^3 to 8192^3 (the blocks per CU of a
+// shape are what its LDS stages allow).
+//   256 x 256  phased, 128 KB of LDS: 4096^3 in 103 us, where 128 x 128 takes
+//              134 (two per CU) or 154 (one per CU, four stages)
+//   128 x 128  four stages, one per CU: when there is at most one tile per CU
+//              (1024 x 4096 x 4096 in 38 us; with two stages 45, 256 x 256 80)
+//   128 x 128  two stages, two per CU: a few tiles per CU and few chunks
+//              (16384 x 512 x 512 in 15.9 us; four stages 19.5, 256 x 256 22.7)
+//   64 x 64    four stages, two per CU: small products
+//              (1024^3 in 9.5 us; 128 x 128 12.8)
+enum class Shape { k256, k128x4, k128x2, k64 };
+struct ShapeInfo {
+  int64_t tile;
+  int per_cu;
+  double chunk_us, shared_us, end_us;
+};
+constexpr ShapeInfo kShapes[] = {
+    {256, 1, 1.50, 0.0, 5.0}, {128, 1, 0.53, 0.0, 3.0}, {128, 2, 0.62, 1.05, 3.0}, {64, 2, 0.30, 0.42, 2.0}};
+constexpr int64_t kCus = 256;
+
 struct Plan {
   Shape shape;
   int splits;
@@ -603,9 +743,12 @@ bool copyable(const Operand& o, int64_t cols) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.ld % 8 == 0 && (cols % 8 == 0 || o.padded);
 }
 
-void shape_size(Shape s, int64_t& bm, int64_t& bn) {
-  bm = s == Shape::k256x256 ? 256 : s == Shape::k128x128 ? 128 : 64;
-  bn = s == Shape::k256x256 ? 256 : 128;
+// Time of n blocks of `chunks` chunks: full rounds of the card, then the rest.
+double blocks_us(const ShapeInfo& s, int64_t n, int64_t chunks) {
+  const double full = static_cast<double>(chunks) * (s.per_cu > 1 ? s.shared_us : s.chunk_us) + s.end_us;
+  const double alone = static_cast<double>(chunks) * s.chunk_us + s.end_us;
+  const int64_t slots = kCus * s.per_cu, rest = n % slots;
+  return static_cast<double>(n / slots) * full + (rest == 0 ? 0.0 : rest <= kCus ? alone : full);
 }
 
 Plan make_plan(const DenseGemm& p) {
@@ -620,23 +763,19 @@ Plan make_plan(const DenseGemm& p) {
   pl.b_bytes = pl.pack_b ? up256(static_cast<size_t>(pl.b_rows) * up8(pl.b_cols) * 2) : 0;
   pl.chunks = (p.K + kChunk - 1) / kChunk;
 
-  // Shape and number of splits of K by the estimated time: rounds of blocks
-  // times a block's chunks, plus the partial sums' way through memory.
+  // Shape and number of splits of K by the estimated time: the blocks, and
+  // with splits the launch that joins them and the partial sums' way to memory
+  // and back.
   double best = 1e30;
-  for (Shape s : {Shape::k256x256, Shape::k128x128, Shape::k64x128}) {
-    int64_t bm, bn;
-    shape_size(s, bm, bn);
-    const int64_t tm = (p.M + bm - 1) / bm, tn = (nb + bn - 1) / bn;
-    // us per chunk of one block with the CU full, blocks per CU
-    const double chunk_us = s == Shape::k256x256 ? 1.45 : s == Shape::k128x128 ? 1.0 : 1.2;
-    const int64_t slots = 256 * (s == Shape::k256x256 ? 1 : s == Shape::k128x128 ? 2 : 3);
+  for (int i = 0; i < 4; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    const int64_t tm = (p.M + s.tile - 1) / s.tile, tn = (nb + s.tile - 1) / s.tile;
     for (int sp = 1; sp <= 32 && sp <= pl.chunks; sp *= 2) {
-      const int64_t rounds = (tm * tn * sp + slots - 1) / slots;
-      double us = rounds * (static_cast<double>((pl.chunks + sp - 1) / sp) * chunk_us + 3.0);
-      if (sp > 1) us += 4.0 + 2.0 * sp * p.M * nb * 4 / 4e6;
+      double us = blocks_us(s, tm * tn * sp, (pl.chunks + sp - 1) / sp);
+      if (sp > 1) us += 4.0 + 2.0 * sp * static_cast<double>(p.M) * nb * 4 / 4e6;
       if (us < best) {
         best = us;
-        pl.shape = s, pl.splits = sp, pl.tiles_m = tm, pl.tiles_n = tn;
+        pl.shape = static_cast<Shape>(i), pl.splits = sp, pl.tiles_m = tm, pl.tiles_n = tn;
       }
     }
   }
@@ -651,19 +790,24 @@ hipError_t pack(const Operand& o, int64_t rows, int64_t cols, uint16_t* dst, hip
   return hipGetLastError();
 }
 
-template <int HM, int HN, int WM, int WN>
-hipError_t launch_shape(const TileArgs& t, hipStream_t s) {
+template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
+hipError_t launch_kernel(const TileArgs& t, hipStream_t s) {
   const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(t.tiles_m) * t.tiles_n * t.splits);
   constexpr int threads = 64 * WM * WN;
-  if (t.p.epi == DenseEpi::kGated)   // forward only: both operands by rows
-    dense_tile_kernel<HM, HN, WM, WN, false, false, DenseEpi::kGated><<<grid, threads, 0, s>>>(t);
-  else if (!t.p.b.k_rows)
-    dense_tile_kernel<HM, HN, WM, WN, false, false, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
-  else if (!t.p.a.k_rows)
-    dense_tile_kernel<HM, HN, WM, WN, false, true, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
+  if constexpr (HM == 128)
+    dense_phased_kernel<HM, HN, WM, WN, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   else
-    dense_tile_kernel<HM, HN, WM, WN, true, true, DenseEpi::kLinear><<<grid, threads, 0, s>>>(t);
+    dense_ring_kernel<HM, HN, WM, WN, S, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   return hipGetLastError();
+}
+
+template <int HM, int HN, int WM, int WN, int S>
+hipError_t launch_shape(const TileArgs& t, hipStream_t s) {
+  if (t.p.epi == DenseEpi::kGated)   // forward only: both operands by rows
+    return launch_kernel<HM, HN, WM, WN, S, false, false, DenseEpi::kGated>(t, s);
+  if (!t.p.b.k_rows) return launch_kernel<HM, HN, WM, WN, S, false, false, DenseEpi::kLinear>(t, s);
+  if (!t.p.a.k_rows) return launch_kernel<HM, HN, WM, WN, S, false, true, DenseEpi::kLinear>(t, s);
+  return launch_kernel<HM, HN, WM, WN, S, true, true, DenseEpi::kLinear>(t, s);
 }
 
 bool row16(const void* p, int64_t ld, int es) {
@@ -712,9 +856,10 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
     t.ldp = gated ? 2 * up8(p.N) : up8(p.N);
   }
   switch (pl.shape) {
-    case Shape::k256x256: e = launch_shape<128, 128, 2, 4>(t, s); break;
-    case Shape::k128x128: e = launch_shape<64, 64, 2, 2>(t, s); break;
-    case Shape::k64x128: e = launch_shape<32, 64, 1, 4>(t, s); break;
+    case Shape::k256: e = launch_shape<128, 128, 2, 4, 2>(t, s); break;
+    case Shape::k128x4: e = launch_shape<64, 64, 2, 4, 4>(t, s); break;
+    case Shape::k128x2: e = launch_shape<64, 64, 2, 4, 2>(t, s); break;
+    case Shape::k64: e = launch_shape<32, 32, 2, 2, 4>(t, s); break;
   }
   if (e != hipSuccess || pl.splits == 1) return e;
   const int64_t blocks = (p.M * (up8(p.N) / 8) + 255) / 256;

@@ -104,16 +104,32 @@ def _vec(t, n, name, device, dtype=None):
 
 
 def _begin(x, name):
-    """The device of x (the current one) and its current stream."""
+    """The device of x (the current one) and its current stream.  The raw
+    stream handle is asked for directly: a torch.cuda.Stream object takes 2.7
+    us to make, as long as the launch itself."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     device = x.device
-    stream = torch.cuda.current_stream()
-    if stream.device != device:
-        raise ValueError(f"{name} is on {device}, but the current device is {stream.device}")
-    return device, stream.cuda_stream
+    index = device.index
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return device, torch._C._cuda_getCurrentRawStream(index)
+
+
+def _new(rows, cols, dtype, device):
+    """(tensor, pointer, row stride) of a new matrix."""
+    t = torch.empty((rows, cols), dtype=dtype, device=device)
+    return t, t.data_ptr(), cols
+
+
+def _out(t, rows, cols, dtype, name, device):
+    """(tensor, pointer, row stride) of an output, allocated if it is None."""
+    if t is None:
+        return _new(rows, cols, dtype, device)
+    p, ld = _mat(t, (rows, cols), None, name, device)
+    return t, p, ld
 
 
 def _act(act):
@@ -148,17 +164,17 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     rp, ldr = _mat(residual, (rows, cols), x.dtype, "residual", device)
     gp, gt = _vec(gamma, cols, "gamma", device)
     bp, pt = _vec(beta, cols, "beta", device, None if gamma is None else gamma.dtype)
-    if y is None:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=device)
-    if total is None and residual is not None:
-        total = torch.empty((rows, cols), dtype=x.dtype, device=device)
-    yp, ldy = _mat(y, (rows, cols), x.dtype, "y", device)
-    sp, lds = _mat(total, (rows, cols), x.dtype, "total", device)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=device)
-    mp = stats.data_ptr()
+    y, yp, ldy = _out(y, rows, cols, x.dtype, "y", device)
+    sp, lds = None, 0
+    if total is not None or residual is not None:
+        total, sp, lds = _out(total, rows, cols, x.dtype, "total", device)
+    if y.dtype != x.dtype or (total is not None and total.dtype != x.dtype):
+        raise TypeError(f"y and total must be {x.dtype}")
+    stats, mp, _ = _new(2, rows, torch.float32, device)
+    mean, rstd = stats.unbind(0)
     _check(lib.dsmoe_layer_norm(xp, ldx, rp, ldr, xt, gp, bp, pt if gp is None else gt, rows, cols, eps, yp, ldy, sp,
                                 lds, mp, mp + 4 * rows, stream), "dsmoe_layer_norm")
-    return y, stats[0], stats[1], total
+    return y, mean, rstd, total
 
 
 def layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -182,15 +198,14 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     mp, _ = _vec(mean, rows, "mean", device, torch.float32)
     rp, _ = _vec(rstd, rows, "rstd", device, torch.float32)
     gp, gt = _vec(gamma, cols, "gamma", device)
-    if dx is None:
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=device)
-    dxp, lddx = _mat(dx, (rows, cols), dy.dtype, "dx", device)
+    dx, dxp, lddx = _out(dx, rows, cols, dy.dtype, "dx", device)
+    if dx.dtype != dy.dtype:
+        raise TypeError(f"dx must be {dy.dtype}")
     dgamma = dbeta = dgp = dbp = None
     keep, wp, wn = None, None, 0
     if need_dparams:
-        params = torch.empty((2, cols), dtype=torch.float32, device=device)
-        dgamma, dbeta = params[0], params[1]
-        dgp = params.data_ptr()
+        params, dgp, _ = _new(2, cols, torch.float32, device)
+        dgamma, dbeta = params.unbind(0)
         dbp = dgp + 4 * cols
         need = lib.dsmoe_layer_norm_backward_workspace_bytes(rows, cols) if workspace is None else 0
         keep, wp, wn = _scratch(workspace, need, device)
@@ -221,13 +236,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     if w.shape[1] != K:
         raise ValueError("x and w must have the same K")
     bp, bt = _vec(bias, N, "bias", device)
-    if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=device)
+    y, yp, ldy = _out(y, M, N, out_dtype, "y", device)
     yt = _dtype_code(y.dtype)
-    yp, ldy = _mat(y, (M, N), None, "y", device)
     rp, ldr = _mat(residual, (M, N), y.dtype, "residual", device)
-    z = torch.empty((M, N), dtype=y.dtype, device=device) if save_z else None
-    zp, ldz = _mat(z, None, None, "z")
+    z, zp, ldz = _new(M, N, y.dtype, device) if save_z else (None, None, 0)
     need = lib.dsmoe_linear_workspace_bytes(xp, ldx, wp, ldw, M, N, K) if workspace is None else 0
     keep, sp, sn = _scratch(workspace, need, device)
     _check(lib.dsmoe_linear(xp, ldx, wp, ldw, bp, bt, rp, ldr, code, M, N, K, yp, ldy, yt, zp, ldz, sp, sn, stream),
@@ -264,20 +276,19 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: Optio
     zt = BF16 if z is None else _dtype_code(z.dtype)
     if code and z is None:
         raise ValueError(f"act {act!r} needs the saved z")
-    if dx is None and need_dx:
-        dx = torch.empty((M, K), dtype=dx_dtype, device=device)
-    if dw is None and need_dw:
-        dw = torch.empty((N, K), dtype=dw_dtype, device=device)
+    dxp, lddx, dxt, dwp, lddw, dwt = None, 0, BF16, None, 0, F32
+    if dx is not None or need_dx:
+        dx, dxp, lddx = _out(dx, M, K, dx_dtype, "dx", device)
+        dxt = _dtype_code(dx.dtype)
+    if dw is not None or need_dw:
+        dw, dwp, lddw = _out(dw, N, K, dw_dtype, "dw", device)
+        dwt = _dtype_code(dw.dtype)
     dbias = torch.empty((N,), dtype=torch.float32, device=device) if need_dbias else None
-    dxp, lddx = _mat(dx, (M, K), None, "dx", device)
-    dwp, lddw = _mat(dw, (N, K), None, "dw", device)
     need = lib.dsmoe_linear_backward_workspace_bytes(dyp, lddy, xp, ldx, wp, ldw, code, M, N, K) \
         if workspace is None else 0
     keep, sp, sn = _scratch(workspace, need, device)
     _check(lib.dsmoe_linear_backward(dyp, lddy, xp, ldx, wp, ldw, zp, ldz, zt, code, M, N, K, dxp, lddx,
-                                     BF16 if dx is None else _dtype_code(dx.dtype), dwp, lddw,
-                                     F32 if dw is None else _dtype_code(dw.dtype),
-                                     None if dbias is None else dbias.data_ptr(), sp, sn, stream),
+                                     dxt, dwp, lddw, dwt, None if dbias is None else dbias.data_ptr(), sp, sn, stream),
            "dsmoe_linear_backward")
     return dx, dw, dbias
 
@@ -303,12 +314,9 @@ def gated_linear(x: torch.Tensor, w13: torch.Tensor, act: str = "silu", out_dtyp
     I = w13.shape[0] // 2
     if w13.shape[1] != H or w13.shape[0] != 2 * I:
         raise ValueError("w13 must be [2I][H] with x's H")
-    if a is None:
-        a = torch.empty((M, I), dtype=out_dtype, device=device)
+    a, ap, lda = _out(a, M, I, out_dtype, "a", device)
     at = _dtype_code(a.dtype)
-    ap, lda = _mat(a, (M, I), None, "a", device)
-    h = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=device) if save_h else None
-    hp, ldh = _mat(h, None, None, "h")
+    h, hp, ldh = _new(M, 2 * I, torch.bfloat16, device) if save_h else (None, None, 0)
     need = lib.dsmoe_gated_linear_workspace_bytes(xp, ldx, wp, ldw, M, H, I) if workspace is None else 0
     keep, sp, sn = _scratch(workspace, need, device)
     _check(lib.dsmoe_gated_linear(xp, ldx, wp, ldw, code, M, H, I, ap, lda, at, hp, ldh, sp, sn, stream),
@@ -340,17 +348,17 @@ def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, 
         raise ValueError("w13 must be [2I][H] with da's I")
     xp, ldx = _mat(x, (M, H), torch.bfloat16, "x", device)
     hp, ldh = _mat(h, (M, 2 * I), torch.bfloat16, "h", device)
-    if dx is None and need_dx:
-        dx = torch.empty((M, H), dtype=dx_dtype, device=device)
-    if dw13 is None and need_dw:
-        dw13 = torch.empty((2 * I, H), dtype=dw_dtype, device=device)
-    dxp, lddx = _mat(dx, (M, H), None, "dx", device)
-    dwp, lddw = _mat(dw13, (2 * I, H), None, "dw13", device)
+    dxp, lddx, dxt, dwp, lddw, dwt = None, 0, BF16, None, 0, F32
+    if dx is not None or need_dx:
+        dx, dxp, lddx = _out(dx, M, H, dx_dtype, "dx", device)
+        dxt = _dtype_code(dx.dtype)
+    if dw13 is not None or need_dw:
+        dw13, dwp, lddw = _out(dw13, 2 * I, H, dw_dtype, "dw13", device)
+        dwt = _dtype_code(dw13.dtype)
     need = lib.dsmoe_gated_linear_backward_workspace_bytes(xp, ldx, wp, ldw, M, H, I) if workspace is None else 0
     keep, sp, sn = _scratch(workspace, need, device)
     _check(lib.dsmoe_gated_linear_backward(dap, ldda, xp, ldx, wp, ldw, hp, ldh, code, M, H, I, dxp, lddx,
-                                           BF16 if dx is None else _dtype_code(dx.dtype), dwp, lddw,
-                                           F32 if dw13 is None else _dtype_code(dw13.dtype), sp, sn, stream),
+                                           dxt, dwp, lddw, dwt, sp, sn, stream),
            "dsmoe_gated_linear_backward")
     return dx, dw13
 
