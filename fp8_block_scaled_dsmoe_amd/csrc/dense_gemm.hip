@@ -714,16 +714,19 @@ __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd
 //              (1024 x 4096 x 4096 in 38 us; with two stages 45, 256 x 256 80)
 //   128 x 128  two stages, two per CU: a few tiles per CU and few chunks
 //              (16384 x 512 x 512 in 15.9 us; four stages 19.5, 256 x 256 22.7)
+//   128 x 256  three stages, one per CU: when 256 x 256 leaves CUs without a
+//              tile (4096 x 2048 x 7168 in 103 us; 128 x 128 117, 256 x 256 173)
 //   64 x 64    four stages, two per CU: small products
 //              (1024^3 in 9.5 us; 128 x 128 12.8)
-enum class Shape { k256, k128x4, k128x2, k64 };
+enum class Shape { k256, k128x256, k128x4, k128x2, k64 };
 struct ShapeInfo {
-  int64_t tile;
+  int64_t rows, cols;
   int per_cu;
   double chunk_us, shared_us, end_us;
 };
 constexpr ShapeInfo kShapes[] = {
-    {256, 1, 1.50, 0.0, 5.0}, {128, 1, 0.53, 0.0, 3.0}, {128, 2, 0.62, 1.05, 3.0}, {64, 2, 0.30, 0.42, 2.0}};
+    {256, 256, 1, 1.50, 0.0, 5.0},  {128, 256, 1, 0.90, 0.0, 4.0}, {128, 128, 1, 0.53, 0.0, 3.0},
+    {128, 128, 2, 0.62, 1.05, 3.0}, {64, 64, 2, 0.30, 0.42, 2.0}};
 constexpr int64_t kCus = 256;
 
 struct Plan {
@@ -767,9 +770,9 @@ Plan make_plan(const DenseGemm& p) {
   // with splits the launch that joins them and the partial sums' way to memory
   // and back.
   double best = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 5; ++i) {
     const ShapeInfo& s = kShapes[i];
-    const int64_t tm = (p.M + s.tile - 1) / s.tile, tn = (nb + s.tile - 1) / s.tile;
+    const int64_t tm = (p.M + s.rows - 1) / s.rows, tn = (nb + s.cols - 1) / s.cols;
     for (int sp = 1; sp <= 32 && sp <= pl.chunks; sp *= 2) {
       double us = blocks_us(s, tm * tn * sp, (pl.chunks + sp - 1) / sp);
       if (sp > 1) us += 4.0 + 2.0 * sp * static_cast<double>(p.M) * nb * 4 / 4e6;
@@ -794,7 +797,7 @@ template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
 hipError_t launch_kernel(const TileArgs& t, hipStream_t s) {
   const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(t.tiles_m) * t.tiles_n * t.splits);
   constexpr int threads = 64 * WM * WN;
-  if constexpr (HM == 128)
+  if constexpr (HM == 128 && HN == 128)
     dense_phased_kernel<HM, HN, WM, WN, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   else
     dense_ring_kernel<HM, HN, WM, WN, S, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
@@ -857,6 +860,7 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   }
   switch (pl.shape) {
     case Shape::k256: e = launch_shape<128, 128, 2, 4, 2>(t, s); break;
+    case Shape::k128x256: e = launch_shape<64, 128, 2, 4, 3>(t, s); break;
     case Shape::k128x4: e = launch_shape<64, 64, 2, 4, 4>(t, s); break;
     case Shape::k128x2: e = launch_shape<64, 64, 2, 4, 2>(t, s); break;
     case Shape::k64: e = launch_shape<32, 32, 2, 2, 4>(t, s); break;

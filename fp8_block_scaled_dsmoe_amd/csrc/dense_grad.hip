@@ -52,84 +52,97 @@ __device__ __forceinline__ u32x4 pack8(const float* v) {
   return a;
 }
 
-// Block (x, y): 256 slots of 8 columns, strip y of the rows.
+// A block takes `ct` slots of 8 columns (a power of 2, 32 at most) and the rows
+// of strip blockIdx.y, 256 / ct of them at a time, two such steps of loads in
+// flight; its threads' column sums are joined through LDS.
 template <bool ZF32>
 __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                                            const void* __restrict__ z, int64_t ldz, bool vec,
-                                                           int act, int64_t M, int64_t N, int64_t strip,
+                                                           int act, int64_t M, int64_t N, int ct, int64_t strip,
                                                            uint16_t* __restrict__ dz, int64_t lddz,
                                                            float* __restrict__ partial) {
-  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
-  if (c >= N) return;
+  __shared__ float s_sum[256 * 8];
+  const int slot = threadIdx.x % ct, rt = 256 / ct;
+  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * ct + slot);
   float sum[8] = {};
   const int64_t r1 = min(M, (blockIdx.y + 1) * strip);
-  for (int64_t r = blockIdx.y * strip; r < r1; ++r) {
-    float g[8];
-    load8<false>(dy + r * lddy, c, N, vec, g);
-    if (z) {
-      float zz[8];
-      load8<ZF32>(static_cast<const char*>(z) + r * ldz * (ZF32 ? 4 : 2), c, N, vec, zz);
+  if (c < N) {
+#pragma unroll 2
+    for (int64_t r = blockIdx.y * strip + threadIdx.x / ct; r < r1; r += rt) {
+      float g[8];
+      load8<false>(dy + r * lddy, c, N, vec, g);
+      if (z) {
+        float zz[8];
+        load8<ZF32>(static_cast<const char*>(z) + r * ldz * (ZF32 ? 4 : 2), c, N, vec, zz);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float f, d;
-        act_and_grad_f32(act, zz[e], f, d);
-        g[e] *= d;
+        for (int e = 0; e < 8; ++e) {
+          float f, d;
+          act_and_grad_f32(act, zz[e], f, d);
+          g[e] *= d;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += g[e];
+      // dz's rows are padded to a multiple of 8 with zeros (the products read
+      // whole groups of 8)
+      if (dz) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e >= N) g[e] = 0.0f;
+        *reinterpret_cast<u32x4*>(dz + r * lddz + c) = pack8(g);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += g[e];
-    // dz's rows are padded to a multiple of 8 with zeros (the products read
-    // whole groups of 8)
-    if (dz) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e >= N) g[e] = 0.0f;
-      *reinterpret_cast<u32x4*>(dz + r * lddz + c) = pack8(g);
-    }
   }
-  if (partial) {
-    float* o = partial + blockIdx.y * N + c;
+  if (!partial) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < N) o[e] = sum[e];
+  for (int e = 0; e < 8; ++e) s_sum[e * 256 + threadIdx.x] = sum[e];
+  __syncthreads();
+  // thread i < 8 ct sums column (i / ct) of slot (i % ct), rows in order
+  if (static_cast<int>(threadIdx.x) < 8 * ct) {
+    const int e = threadIdx.x / ct;
+    const int64_t col = 8 * (static_cast<int64_t>(blockIdx.x) * ct + slot) + e;
+    float s = 0.0f;
+    for (int r = 0; r < rt; ++r) s += s_sum[e * 256 + r * ct + slot];
+    if (col < N) partial[blockIdx.y * N + col] = s;
   }
 }
 
-// Block (x, y): 256 slots of 8 columns of da, strip y of the rows.
+// One slot of 8 columns of da per thread.
 __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __restrict__ da, int64_t ldda,
                                                              const uint16_t* __restrict__ h, int64_t ldh, bool vec,
-                                                             int act, int64_t M, int64_t I, int64_t strip,
+                                                             int act, int64_t M, int64_t I,
                                                              uint16_t* __restrict__ dh, int64_t lddh) {
-  const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
-  if (c >= I) return;
-  const int64_t r1 = min(M, (blockIdx.y + 1) * strip);
-  for (int64_t r = blockIdx.y * strip; r < r1; ++r) {
-    float d[8], g[8], u[8], dg[8], du[8];
-    load8<false>(da + r * ldda, c, I, vec, d);
-    load8<false>(h + r * ldh, c, I, vec, g);
-    load8<false>(h + r * ldh + I, c, I, vec, u);
+  const uint32_t slots = static_cast<uint32_t>((I + 7) / 8);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= M * slots) return;
+  // 32-bit division where the index allows it
+  const int64_t r = i >> 32 ? i / slots : static_cast<uint32_t>(i) / slots;
+  const int64_t c = 8 * (i - r * slots);
+  float d[8], g[8], u[8], dg[8], du[8];
+  load8<false>(da + r * ldda, c, I, vec, d);
+  load8<false>(h + r * ldh, c, I, vec, g);
+  load8<false>(h + r * ldh + I, c, I, vec, u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float f, df;
-      act_and_grad_f32(act, g[e], f, df);
-      dg[e] = d[e] * u[e] * df;
-      du[e] = d[e] * f;
-    }
-    uint16_t* o = dh + r * lddh + c;
-    if (vec) {
-      *reinterpret_cast<u32x4*>(o) = pack8(dg);
-      *reinterpret_cast<u32x4*>(o + I) = pack8(du);
-    } else {
+  for (int e = 0; e < 8; ++e) {
+    float f, df;
+    act_and_grad_f32(act, g[e], f, df);
+    dg[e] = d[e] * u[e] * df;
+    du[e] = d[e] * f;
+  }
+  uint16_t* o = dh + r * lddh + c;
+  if (vec) {
+    *reinterpret_cast<u32x4*>(o) = pack8(dg);
+    *reinterpret_cast<u32x4*>(o + I) = pack8(du);
+  } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < I) {
-          o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
-          o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
-        }
-      // the row's padding past 2 I, by the thread that owns the last column
-      if (c + 8 >= I)
-        for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
-    }
+    for (int e = 0; e < 8; ++e)
+      if (c + e < I) {
+        o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
+        o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
+      }
+    // the row's padding past 2 I, by the thread that owns the last column
+    if (c + 8 >= I)
+      for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
   }
 }
 
@@ -137,26 +150,39 @@ bool row16(const void* p, int64_t ld, int es) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
 }
 
-// rows per strip: 16 or more, with at most 256 strips
-int64_t strip_rows(int64_t M) {
-  const int64_t s = (M + 255) / 256;
-  return s < 16 ? 16 : s;
+// column slots of a block of act_backward_kernel, rows of a strip: about 1024
+// blocks, of at least two steps of rows each
+int column_slots(int64_t N) {
+  int ct = 1;
+  while (ct < 32 && ct * 8 < N) ct *= 2;
+  return ct;
+}
+int64_t strip_rows(int64_t M, int64_t N) {
+  const int ct = column_slots(N);
+  const int64_t blocks_n = (N + 8 * ct - 1) / (8 * ct), step = 256 / ct;
+  const int64_t strips = (1024 + blocks_n - 1) / blocks_n, least = (M + 65534) / 65535;   // the grid's limit
+  const int64_t rows = (M + strips - 1) / strips;
+  const int64_t s = rows < 2 * step ? 2 * step : rows;
+  return s < least ? least : s;
 }
 
 }  // namespace
 
-int64_t bias_partial_rows(int64_t M, int64_t N) { return M == 0 ? 0 : (M + strip_rows(M) - 1) / strip_rows(M); }
+int64_t bias_partial_rows(int64_t M, int64_t N) {
+  return M == 0 ? 0 : (M + strip_rows(M, N) - 1) / strip_rows(M, N);
+}
 
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz, bool z_f32, int act,
                                int64_t M, int64_t N, uint16_t* dz, int64_t lddz, float* partial, hipStream_t s) {
   if (M == 0) return hipSuccess;
   const bool vec = N % 8 == 0 && row16(dy, lddy, 2) && row16(z, ldz, z_f32 ? 4 : 2);
-  const int64_t strip = strip_rows(M);
-  const dim3 grid(static_cast<uint32_t>((N + 2047) / 2048), static_cast<uint32_t>((M + strip - 1) / strip));
+  const int ct = column_slots(N);
+  const int64_t strip = strip_rows(M, N);
+  const dim3 grid(static_cast<uint32_t>((N + 8 * ct - 1) / (8 * ct)), static_cast<uint32_t>((M + strip - 1) / strip));
   if (z_f32)
-    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, strip, dz, lddz, partial);
+    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, ct, strip, dz, lddz, partial);
   else
-    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, strip, dz, lddz, partial);
+    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, ct, strip, dz, lddz, partial);
   return hipGetLastError();
 }
 
@@ -164,9 +190,8 @@ hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_
                                  int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s) {
   if (M == 0) return hipSuccess;
   const bool vec = I % 8 == 0 && row16(da, ldda, 2) && row16(h, ldh, 2);
-  const int64_t strip = strip_rows(M);
-  const dim3 grid(static_cast<uint32_t>((I + 2047) / 2048), static_cast<uint32_t>((M + strip - 1) / strip));
-  gated_backward_kernel<<<grid, 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, strip, dh, lddh);
+  const int64_t blocks = (M * ((I + 7) / 8) + 255) / 256;
+  gated_backward_kernel<<<static_cast<uint32_t>(blocks), 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, dh, lddh);
   return hipGetLastError();
 }
 

@@ -37,35 +37,50 @@ struct Row {
   static __device__ __forceinline__ int64_t col(int v, int e, int t) {
     return VEC ? 8 * (static_cast<int64_t>(v) * NT + t) + e : (8 * static_cast<int64_t>(v) + e) * NT + t;
   }
-  // slot v of the row at base (8 values; those past cols read 0)
-  static __device__ __forceinline__ void load(const void* base, int v, int t, int64_t cols, float* o) {
+  // 8 values as loaded: bf16 pairs, or float32
+  struct Raw {
+    u32x4 q[F32 ? 2 : 1];
+  };
+  // slot v of the row at base (those past cols read 0)
+  static __device__ __forceinline__ Raw fetch(const void* base, int v, int t, int64_t cols) {
+    Raw r;
     if constexpr (VEC) {
       const int64_t c = col(v, 0, t);
-      if (c < cols) {
-        if constexpr (F32) {
-          const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + c);
-          const f32x4 a = q[0], b = q[1];
+      const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const char*>(base) + c * (F32 ? 4 : 2));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
-        } else {
-          const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[2 * e] = __uint_as_float(a[e] << 16);
-            o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-      }
-    } else {
+      for (int h = 0; h < (F32 ? 2 : 1); ++h) r.q[h] = c < cols ? q[h] : u32x4{0, 0, 0, 0};
+    } else if constexpr (F32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int64_t c = col(v, e, t);
-        o[e] = c < cols ? load1(base, c, F32) : 0.0f;
+        r.q[e / 4][e % 4] = c < cols ? static_cast<const uint32_t*>(base)[c] : 0;
+      }
+    } else {
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c = col(v, e, t);
+        h[e] = c < cols ? static_cast<const uint16_t*>(base)[c] : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.q[0][e] = h[2 * e] | h[2 * e + 1] << 16;
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* o) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(r.q[e / 4][e % 4]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[2 * e] = __uint_as_float(r.q[0][e] << 16);
+        o[2 * e + 1] = __uint_as_float(r.q[0][e] & 0xffff0000u);
       }
     }
+  }
+  static __device__ __forceinline__ void load(const void* base, int v, int t, int64_t cols, float* o) {
+    unpack(fetch(base, v, t, cols), o);
   }
   static __device__ __forceinline__ void store(void* base, int v, int t, int64_t cols, const float* o) {
     if constexpr (VEC) {
@@ -309,21 +324,39 @@ __global__ __launch_bounds__(bwd_threads(NT)) void layer_norm_bwd_kernel(NormBwd
 #pragma unroll
     for (int e = 0; e < 8; ++e) dga[v][e] = dbe[v][e] = 0.0f;
   }
-  int flip = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RG; r0 < p.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * RG, flip ^= 1) {
-    const int64_t row = r0 + rg;
-    const bool live = row < p.rows;   // the same for a row's NT threads
-    float x[PER][8], dy[PER][8], sums[2] = {0.0f, 0.0f};
-    float mean = 0.0f, rstd = 0.0f;
-    if (live) {
-      mean = p.mean[row];
-      rstd = p.rstd[row];
+  // The next row is fetched before this one is finished: with the loads of a
+  // row waited for in turn, two blocks per CU kept too few bytes on the way
+  // (4096 x 7168 bf16 with dsum took 103 us).
+  typename R::Raw nx[PER], ny[PER], nd[PER];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= p.rows) return;   // the same for a row's NT threads
+    nmean = p.mean[row];
+    nrstd = p.rstd[row];
 #pragma unroll
-      for (int v = 0; v < PER; ++v) {
-        R::load(static_cast<const char*>(p.x) + row * p.ldx * ES, v, t, cols, x[v]);
-        R::load(static_cast<const char*>(p.dy) + row * p.lddy * ES, v, t, cols, dy[v]);
-      }
+    for (int v = 0; v < PER; ++v) {
+      nx[v] = R::fetch(static_cast<const char*>(p.x) + row * p.ldx * ES, v, t, cols);
+      ny[v] = R::fetch(static_cast<const char*>(p.dy) + row * p.lddy * ES, v, t, cols);
+      if (p.dsum) nd[v] = R::fetch(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols);
+    }
+  };
+  int flip = 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * RG;
+  fetch(static_cast<int64_t>(blockIdx.x) * RG + rg);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RG; r0 < p.rows; r0 += stride, flip ^= 1) {
+    const int64_t row = r0 + rg;
+    const bool live = row < p.rows;
+    float x[PER][8], dy[PER][8], sums[2] = {0.0f, 0.0f};
+    typename R::Raw ds[PER];
+    const float mean = nmean, rstd = nrstd;
+#pragma unroll
+    for (int v = 0; v < PER; ++v) {
+      R::unpack(nx[v], x[v]);
+      R::unpack(ny[v], dy[v]);
+      ds[v] = nd[v];
+    }
+    fetch(row + stride);
+    if (live) {
 #pragma unroll
       for (int v = 0; v < PER; ++v)
 #pragma unroll
@@ -340,13 +373,16 @@ __global__ __launch_bounds__(bwd_threads(NT)) void layer_norm_bwd_kernel(NormBwd
     const float c1 = sums[0] * inv, c2 = sums[1] * inv;
 #pragma unroll
     for (int v = 0; v < PER; ++v) {
-      float o[8], ds[8];
+      float o[8], d[8];
+      if (p.dsum) {
+        R::unpack(ds[v], d);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ds[e] = 0.0f;
-      if (p.dsum) R::load(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols, ds);
+        for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = __builtin_fmaf(rstd, dy[v][e] * ga[v][e] - c1 - x[v][e] * c2, ds[e]);
+        o[e] = __builtin_fmaf(rstd, dy[v][e] * ga[v][e] - c1 - x[v][e] * c2, d[e]);
         dga[v][e] = __builtin_fmaf(dy[v][e], x[v][e], dga[v][e]);
         dbe[v][e] += dy[v][e];
       }
@@ -436,17 +472,19 @@ __global__ __launch_bounds__(256) void layer_norm_wgrad_long_kernel(NormBwd p) {
   out[p.cols + c] = dbe;
 }
 
-// out[c] = sum over r < n of partial[r][c]: 64 columns per block, wave w sums
-// a quarter of the rows, 8 loads in flight; the quarters are joined in order.
-__global__ __launch_bounds__(256) void sum_partials_kernel(const float* __restrict__ partial, int64_t n, int64_t cols,
-                                                           int64_t split, float* __restrict__ out0,
-                                                           float* __restrict__ out1) {
-  __shared__ float s_sum[4][64];
+// out[c] = sum over r < n of partial[r][c]: 64 columns per block, each of 16
+// waves sums a 16th of the rows, 8 loads in flight; joined in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void sum_partials_kernel(const float* __restrict__ partial, int64_t n,
+                                                                      int64_t cols, int64_t split,
+                                                                      float* __restrict__ out0,
+                                                                      float* __restrict__ out1) {
+  __shared__ float s_sum[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   float acc = 0.0f;
   if (c < cols) {
-    const int64_t per = (n + 3) / 4, r1 = min(n, (w + 1) * per);
+    const int64_t per = (n + kSumWaves - 1) / kSumWaves, r1 = min(n, (w + 1) * per);
     int64_t r = w * per;
     for (; r + 8 <= r1; r += 8) {
       float v[8];
@@ -460,14 +498,17 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(const float* __restri
   s_sum[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < cols) {
-    const float s = ((s_sum[0][lane] + s_sum[1][lane]) + s_sum[2][lane]) + s_sum[3][lane];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumWaves; ++i) s += s_sum[i][lane];
     (c < split ? out0[c] : out1[c - split]) = s;
   }
 }
 
 hipError_t sum_partials(const float* partial, int64_t n, int64_t cols, int64_t split, float* o0, float* o1,
                         hipStream_t s) {
-  sum_partials_kernel<<<static_cast<uint32_t>((cols + 63) / 64), 256, 0, s>>>(partial, n, cols, split, o0, o1);
+  sum_partials_kernel<<<static_cast<uint32_t>((cols + 63) / 64), 64 * kSumWaves, 0, s>>>(partial, n, cols, split, o0,
+                                                                                       o1);
   return hipGetLastError();
 }
 
