@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsmoe.so")
 SOURCES = ["abi.hip", "quant.hip", "granularity.hip", "serving.hip", "route.hip", "gemm.hip", "backward.hip",
-           "norm.hip", "dense_grad.hip", "dense_gemm.hip", "dense_abi.hip"]
+           "norm.hip", "dense_grad.hip", "dense_gemm.hip", "dense_skinny.hip", "dense_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

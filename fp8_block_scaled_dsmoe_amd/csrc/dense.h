@@ -90,6 +90,10 @@ struct DenseGemm {
 size_t dense_gemm_workspace_bytes(const DenseGemm& p);
 hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s);
 
+// dense_skinny.hip: the same products for p.M <= 64 and both operands by rows;
+// no workspace
+hipError_t launch_dense_skinny(const DenseGemm& p, hipStream_t s);
+
 // dst [M][N] (row stride ldd, type f32 / bf16) = 0
 hipError_t launch_zero_matrix(void* dst, int64_t ldd, bool f32, int64_t m, int64_t n, hipStream_t s);
 

@@ -110,6 +110,7 @@ struct TileArgs {
   int64_t a_k, b_k;       // contraction length readable along a row (row operands: a multiple of 8)
   int64_t a_r, b_r;       // rows readable (k-row operands: a multiple of 8; kGated: of one half of b)
   bool vec;               // every matrix of the epilogue takes vector accesses
+  bool plain;             // kLinear: one split, no activation or z, whole vectors
   float* partial;         // splits > 1: [split][M][ldp] partial sums, no epilogue
   int64_t ldp;            // (kGated: gate sums, then up sums at + N rounded up to 8)
   int32_t splits;
@@ -420,15 +421,102 @@ struct Tile {
         for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
+  // The results pass through LDS, half of the tile's rows at a time, so that a
+  // thread finishes runs of 8 columns and a wave writes whole lines.
+  static constexpr int kRuns = (kGated ? HN : 2 * HN) / 8;   // of 8 columns
+  static constexpr int kRowsAtOnce = 64 * NW / kRuns < HM ? 64 * NW / kRuns : HM;
+  static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
+
+  // Half ha of the results to LDS.  A result lane holds row l % 16 of its A
+  // fragment and columns 4 (l / 16) + [0, 4) of its B fragment; rows 16 bytes
+  // off a multiple of 256 apart keep the writes of 16 rows on separate banks.
+  __device__ __forceinline__ void put(const f32x4 (&acc)[2][TM][TN]) const {
+    wait_lds();        // this wave's reads of LDS are done, and past the barrier
+    block_barrier();   // everyone's
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int r = wm * (HM / WM) + 16 * i + (lane & 15);
+          const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
+          *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[hb][i][j];
+        }
+    wait_lds();
+    block_barrier();
+  }
+  __device__ __forceinline__ void get(int r, int col, float* v) const {
+    const uint32_t at = lds + (r * kOutStride + col) * 4;
+    const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
+  }
+
+  // y = acc + bias + residual with whole aligned runs.  The residual of all of
+  // a thread's rows is on its way before the results are in LDS (bf16: of both
+  // halves; a batch of four rows at a time between the stores cost 4096 x 7168
+  // x 2048 with a residual 27 us over the same without).
+  template <bool F32>
+  __device__ __forceinline__ void finish_plain(const Acc& acc) const {
+    constexpr int R = HM / kRowsAtOnce, Q = F32 ? 2 : 1, ES = F32 ? 4 : 2;
+    const int run = threadIdx.x % kRuns, r0 = threadIdx.x / kRuns;
+    const int64_t n = n0 + run * 8;
+    const bool in = n < p.N && r0 < HM;
+    float bias[8];
+    load_bias(p, n, bias);
+    u32x4 res[2][R][Q];
+    auto fetch = [&](int ha) {
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int64_t m = m0 + ha * HM + r0 + q * kRowsAtOnce;
+#pragma unroll
+        for (int h = 0; h < Q; ++h) res[ha][q][h] = u32x4{0, 0, 0, 0};
+        if (p.residual && in && m < p.M) {
+          const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const char*>(p.residual) + (m * p.ldr + n) * ES);
+#pragma unroll
+          for (int h = 0; h < Q; ++h) res[ha][q][h] = from[h];
+        }
+      }
+    };
+    fetch(0);
+    if constexpr (!F32) fetch(1);
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha) {
+      if (F32 && ha == 1) fetch(1);
+      put(acc[ha]);
+      if (!in) continue;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int r = r0 + q * kRowsAtOnce;
+        const int64_t m = m0 + ha * HM + r;
+        if (m >= p.M) break;
+        float v[8];
+        get(r, run * 8, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x;
+          if constexpr (F32)
+            x = __uint_as_float(res[ha][q][e / 4][e % 4]);
+          else
+            x = __uint_as_float(e % 2 ? res[ha][q][0][e / 2] & 0xffff0000u : res[ha][q][0][e / 2] << 16);
+          v[e] = v[e] + bias[e] + x;
+        }
+        store8(p.y, m * p.ldy + n, F32, true, 8, v);
+      }
+    }
+  }
+
   __device__ __forceinline__ void finish(const Acc& acc) const {
-    // The results pass through LDS, half of the tile's rows at a time, so that a
-    // thread finishes runs of 8 columns and a wave writes whole lines.  A result
-    // lane holds row l % 16 of its A fragment and columns 4 (l / 16) + [0, 4) of
-    // its B fragment; rows 16 bytes off a multiple of 256 apart keep the writes
-    // of 16 rows on separate banks.
-    constexpr int kRuns = (kGated ? HN : 2 * HN) / 8;   // of 8 columns
-    constexpr int kRowsAtOnce = 64 * NW / kRuns < HM ? 64 * NW / kRuns : HM;
-    static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
+    if constexpr (!kGated) {
+      if (t.plain) {
+        if (p.y_f32)
+          finish_plain<true>(acc);
+        else
+          finish_plain<false>(acc);
+        return;
+      }
+    }
     const int run = threadIdx.x % kRuns;
     const int64_t n = n0 + run * 8;
     const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
@@ -436,61 +524,25 @@ struct Tile {
     if (!kGated && t.splits == 1) load_bias(p, n, bias);
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
-      block_barrier();   // LDS is free (the last reads were waited for)
-#pragma unroll
-      for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            const int r = wm * (HM / WM) + 16 * i + (lane & 15);
-            const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
-            *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[ha][hb][i][j];
-          }
-      wait_lds();
-      block_barrier();
-      // kBatch rows at a time, their residuals loaded first: one row's residual
-      // at a time left each row waiting for memory in turn
-      constexpr int kBatch = HM / kRowsAtOnce % 4 == 0 ? 4 : HM / kRowsAtOnce % 2 == 0 ? 2 : 1;
-      const int64_t row0 = m0 + ha * HM;
+      put(acc[ha]);
 #pragma unroll 1
-      for (int r0 = threadIdx.x / kRuns; r0 < HM; r0 += kBatch * kRowsAtOnce) {
-        if (row0 + r0 >= p.M || n >= half_n) break;
-        float res[kBatch][8];
+      for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
+        const int64_t m = m0 + ha * HM + r;
+        if (m >= p.M || n >= half_n) break;
+        float v[8], u[8], res[8];
         const bool has_res = !kGated && t.splits == 1 && p.residual && n < p.N;
-        if (has_res) {
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const int64_t m = row0 + r0 + q * kRowsAtOnce;
-            if (m < p.M) load_residual(p, t.vec, m, n, res[q]);
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int r = r0 + q * kRowsAtOnce;
-          const int64_t m = row0 + r;
-          if (m >= p.M) break;
-          const uint32_t at = lds + (r * kOutStride + run * 8) * 4;
-          float v[8], u[8];
-          const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
-          if constexpr (kGated) {
-            const f32x4 u0 = *lds_ptr<const f32x4>(at + HN * 4), u1 = *lds_ptr<const f32x4>(at + HN * 4 + 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = u0[e], u[4 + e] = u1[e];
-          }
-          if (t.splits > 1) {
-            store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
-            if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
-          } else if constexpr (kGated) {
-            finish_gated(p, t.vec, m, n, v, u);
-          } else if (n < p.N) {
-            finish_linear(p, t.vec, m, n, v, bias, has_res, res[q]);
-          }
+        if (has_res) load_residual(p, t.vec, m, n, res);
+        get(r, run * 8, v);
+        if constexpr (kGated) get(r, HN + run * 8, u);
+        if (t.splits > 1) {
+          store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
+          if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
+        } else if constexpr (kGated) {
+          finish_gated(p, t.vec, m, n, v, u);
+        } else if (n < p.N) {
+          finish_linear(p, t.vec, m, n, v, bias, has_res, res);
         }
       }
-      wait_lds();
     }
   }
 };
@@ -728,6 +780,7 @@ constexpr ShapeInfo kShapes[] = {
     {256, 256, 1, 1.50, 0.0, 5.0},  {128, 256, 1, 0.90, 0.0, 4.0}, {128, 128, 1, 0.53, 0.0, 3.0},
     {128, 128, 2, 0.62, 1.05, 3.0}, {64, 64, 2, 0.30, 0.42, 2.0}};
 constexpr int64_t kCus = 256;
+constexpr double kHbm = 4.8e6;   // bytes per us of a long read
 
 struct Plan {
   Shape shape;
@@ -736,7 +789,12 @@ struct Plan {
   bool pack_a, pack_b;
   int64_t a_rows, a_cols, b_rows, b_cols;   // of the stored matrices
   size_t a_bytes, b_bytes, partial_bytes;
+  double us;   // estimated time
 };
+
+bool row16(const void* p, int64_t ld, int es) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
+}
 
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -782,6 +840,11 @@ Plan make_plan(const DenseGemm& p) {
       }
     }
   }
+  // launches, W's way from memory, copies of operands
+  const double bytes = static_cast<double>(nb) * p.K * 2;
+  pl.us = 3.5 + (best > bytes / kHbm ? best + 0.25 * bytes / kHbm : bytes / kHbm + 0.25 * best);
+  if (pl.pack_a) pl.us += 3.0 + 2.0 * pl.a_bytes / kHbm;
+  if (pl.pack_b) pl.us += 3.0 + 2.0 * pl.b_bytes / kHbm;
   pl.partial_bytes = pl.splits > 1 ? static_cast<size_t>(pl.splits) * p.M * (gated ? 2 * up8(p.N) : up8(p.N)) * 4 : 0;
   return pl;
 }
@@ -813,8 +876,20 @@ hipError_t launch_shape(const TileArgs& t, hipStream_t s) {
   return launch_kernel<HM, HN, WM, WN, S, true, true, DenseEpi::kLinear>(t, s);
 }
 
-bool row16(const void* p, int64_t ld, int es) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
+// Whether the kernel for few tokens takes a product.  Its time is W's way from
+// memory or x's way from L2 to every block (about 35 KB per us and CU),
+// whichever is longer, and some of the other; unaligned rows are read value by
+// value.  4096 x 7168: 1 token 12 us (tiles 18), 16 tokens 16 (19), 32 tokens
+// 22 (19); 1000 x 1000: 64 tokens 6.5 (9).
+bool few_tokens(const DenseGemm& p, const Plan& pl) {
+  if (p.M > 64 || p.a.k_rows || p.b.k_rows) return false;
+  const bool gated = p.epi == DenseEpi::kGated;
+  const int64_t blocks = gated ? (p.N + 7) / 8 : (p.N + 15) / 16, groups = (p.M + 15) / 16;
+  const double slow = row16(p.a.p, p.a.ld, 2) && row16(p.b.p, p.b.ld, 2) ? 1.0 : 3.0;
+  const double w = slow * (gated ? 2.0 : 1.0) * p.N * p.K * 2 / kHbm;
+  const double rounds = blocks > kCus ? static_cast<double>(blocks) / kCus : 1.0;
+  const double x = p.M == 1 ? 0.0 : slow * rounds * groups * 16 * p.K * 2 / 35e3;
+  return 4.0 + (w > x ? w + 0.3 * x : x + 0.3 * w) < pl.us;
 }
 
 }  // namespace
@@ -823,11 +898,13 @@ bool operand_copyable(const Operand& o, int64_t cols) { return copyable(o, cols)
 
 size_t dense_gemm_workspace_bytes(const DenseGemm& p) {
   const Plan pl = make_plan(p);
+  if (few_tokens(p, pl)) return 0;
   return pl.a_bytes + pl.b_bytes + up256(pl.partial_bytes);
 }
 
 hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   const Plan pl = make_plan(p);
+  if (few_tokens(p, pl)) return launch_dense_skinny(p, s);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   TileArgs t{};
   t.p = p;
@@ -851,6 +928,7 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   t.vec = row16(p.y, p.ldy, p.y_f32 ? 4 : 2) && row16(p.residual, p.ldr, p.y_f32 ? 4 : 2) &&
           row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && (!gated || !p.z || p.N % 8 == 0);
   t.splits = pl.splits;
+  t.plain = pl.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec && p.N % 8 == 0;
   t.chunks = static_cast<int32_t>(pl.chunks);
   t.tiles_m = static_cast<int32_t>(pl.tiles_m);
   t.tiles_n = static_cast<int32_t>(pl.tiles_n);
