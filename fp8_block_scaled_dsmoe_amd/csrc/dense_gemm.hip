@@ -26,6 +26,7 @@
 #include "act.h"
 #include "common.h"
 #include "dense.h"
+#include "dense_epi.h"
 
 namespace dsmoe {
 namespace {
@@ -50,58 +51,33 @@ constexpr int kXcds = 8;
 // Epilogue: 8 adjacent columns of one row.
 // ---------------------------------------------------------------------------
 
-// columns i .. i + 7 of a matrix at base (f32 or bf16), of which `valid`
-// exist; vec: all 8 do and the accesses are 16-byte aligned
-__device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, bool vec, int valid, float* o) {
+// columns i .. i + 7 of a matrix at base (f32 or bf16), 16-byte accesses
+__device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, float* o) {
   if (f32) {
-    const float* q = static_cast<const float*>(base) + i;
-    if (vec) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(q), b = *reinterpret_cast<const f32x4*>(q + 4);
+    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
+    const f32x4 a = q[0], b = q[1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = e < valid ? q[e] : 0.0f;
-    }
+    for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
   } else {
-    const uint16_t* q = static_cast<const uint16_t*>(base) + i;
-    if (vec) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(q);
+    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[2 * e] = __uint_as_float(a[e] << 16);
-        o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = e < valid ? bf16_to_f32(q[e]) : 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      o[2 * e] = __uint_as_float(a[e] << 16);
+      o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
     }
   }
 }
 
-__device__ __forceinline__ void store8(void* base, int64_t i, bool f32, bool vec, int valid, const float* v) {
+__device__ __forceinline__ void store8(void* base, int64_t i, bool f32, const float* v) {
   if (f32) {
-    float* q = static_cast<float*>(base) + i;
-    if (vec) {
-      *reinterpret_cast<f32x4*>(q) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < valid) q[e] = v[e];
-    }
+    f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + i);
+    q[0] = f32x4{v[0], v[1], v[2], v[3]};
+    q[1] = f32x4{v[4], v[5], v[6], v[7]};
   } else {
-    uint16_t* q = static_cast<uint16_t*>(base) + i;
-    if (vec) {
-      u32x4 a;
+    u32x4 a;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-      *reinterpret_cast<u32x4*>(q) = a;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < valid) q[e] = static_cast<uint16_t>(f32x2_to_bf16x2(v[e], 0.0f));
-    }
+    for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + i) = a;
   }
 }
 
@@ -109,7 +85,7 @@ struct TileArgs {
   DenseGemm p;
   int64_t a_k, b_k;       // contraction length readable along a row (row operands: a multiple of 8)
   int64_t a_r, b_r;       // rows readable (k-row operands: a multiple of 8; kGated: of one half of b)
-  bool vec;               // every matrix of the epilogue takes vector accesses
+  bool vec;               // every matrix of the epilogue takes 16-byte accesses, in whole runs of 8 columns
   bool plain;             // kLinear: one split, no activation or z, whole vectors
   float* partial;         // splits > 1: [split][M][ldp] partial sums, no epilogue
   int64_t ldp;            // (kGated: gate sums, then up sums at + N rounded up to 8)
@@ -118,43 +94,34 @@ struct TileArgs {
   int32_t tiles_m, tiles_n;
 };
 
-__device__ __forceinline__ void load_residual(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* r) {
-  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
-  load8(p.residual, m * p.ldr + n, p.y_f32, pvec && valid == 8, valid, r);
-}
-
-// y = act(acc + bias) + residual (r, when has_res), z = acc + bias
-__device__ __forceinline__ void finish_linear(const DenseGemm& p, bool pvec, int64_t m, int64_t n, float* v,
-                                              const float* bias, bool has_res, const float (&r)[8]) {
-  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
-  const bool vec = pvec && valid == 8;
+// Whole runs of 8 columns: y = act(acc + bias) + residual, z = acc + bias
+__device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int64_t n, float* v, const float* bias) {
+  float r[8];
+  if (p.residual) load8(p.residual, m * p.ldr + n, p.y_f32, r);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] += bias[e];
-  if (p.z) store8(p.z, m * p.ldz + n, p.y_f32, vec, valid, v);
+  if (p.z) store8(p.z, m * p.ldz + n, p.y_f32, v);
   if (p.act != DSMOE_ACT_NONE) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, v[e]);
   }
-  if (has_res) {
+  if (p.residual) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  store8(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+  store8(p.y, m * p.ldy + n, p.y_f32, v);
 }
 
 // a = act(g) u, h = [g | u]
-__device__ __forceinline__ void finish_gated(const DenseGemm& p, bool pvec, int64_t m, int64_t n, const float* g,
-                                             const float* u) {
-  const int valid = static_cast<int>(min(static_cast<int64_t>(8), p.N - n));
-  const bool vec = pvec && valid == 8;
+__device__ __forceinline__ void finish_gated(const DenseGemm& p, int64_t m, int64_t n, const float* g, const float* u) {
   if (p.z) {
-    store8(p.z, m * p.ldz + n, false, vec, valid, g);
-    store8(p.z, m * p.ldz + p.N + n, false, vec, valid, u);
+    store8(p.z, m * p.ldz + n, false, g);
+    store8(p.z, m * p.ldz + p.N + n, false, u);
   }
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, g[e]) * u[e];
-  store8(p.y, m * p.ldy + n, p.y_f32, vec, valid, v);
+  store8(p.y, m * p.ldy + n, p.y_f32, v);
 }
 
 __device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* o) {
@@ -502,7 +469,7 @@ struct Tile {
             x = __uint_as_float(e % 2 ? res[ha][q][0][e / 2] & 0xffff0000u : res[ha][q][0][e / 2] << 16);
           v[e] = v[e] + bias[e] + x;
         }
-        store8(p.y, m * p.ldy + n, F32, true, 8, v);
+        store8(p.y, m * p.ldy + n, F32, v);
       }
     }
   }
@@ -517,30 +484,58 @@ struct Tile {
         return;
       }
     }
+    const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
+    const bool runs = t.splits > 1 || t.vec;
     const int run = threadIdx.x % kRuns;
     const int64_t n = n0 + run * 8;
-    const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
     float bias[8] = {};
-    if (!kGated && t.splits == 1) load_bias(p, n, bias);
+    if (!kGated && t.splits == 1 && t.vec) load_bias(p, n, bias);
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
       put(acc[ha]);
+      if (runs) {
 #pragma unroll 1
-      for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
-        const int64_t m = m0 + ha * HM + r;
-        if (m >= p.M || n >= half_n) break;
-        float v[8], u[8], res[8];
-        const bool has_res = !kGated && t.splits == 1 && p.residual && n < p.N;
-        if (has_res) load_residual(p, t.vec, m, n, res);
-        get(r, run * 8, v);
-        if constexpr (kGated) get(r, HN + run * 8, u);
-        if (t.splits > 1) {
-          store8(t.partial, (split * p.M + m) * t.ldp + n, true, true, 8, v);
-          if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, true, 8, u);
-        } else if constexpr (kGated) {
-          finish_gated(p, t.vec, m, n, v, u);
-        } else if (n < p.N) {
-          finish_linear(p, t.vec, m, n, v, bias, has_res, res);
+        for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
+          const int64_t m = m0 + ha * HM + r;
+          if (m >= p.M || n >= half_n) break;
+          float v[8], u[8];
+          get(r, run * 8, v);
+          if constexpr (kGated) get(r, HN + run * 8, u);
+          if (t.splits > 1) {
+            store8(t.partial, (split * p.M + m) * t.ldp + n, true, v);
+            if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, u);
+          } else if constexpr (kGated) {
+            finish_gated(p, m, n, v, u);
+          } else {
+            finish_linear(p, m, n, v, bias);
+          }
+        }
+      } else {
+        // rows of no alignment: one column per thread, adjacent lanes adjacent
+        // columns, the residuals of kBatch rows loaded first
+        constexpr int kCols = kRuns * 8, kRows = 64 * NW / kCols, kBatch = HM / kRows < 4 ? HM / kRows : 4;
+        static_assert(64 * NW % kCols == 0 && HM % (kRows * kBatch) == 0, "whole batches");
+        const int c = threadIdx.x % kCols;
+        if (n0 + c >= p.N) continue;
+#pragma unroll 1
+        for (int r0 = threadIdx.x / kCols; r0 < HM; r0 += kRows * kBatch) {
+          const int64_t m1 = m0 + ha * HM + r0;
+          float res[kBatch];
+          if (!kGated && p.residual) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+              res[q] = m1 + q * kRows < p.M ? load1(p.residual, (m1 + q * kRows) * p.ldr + n0 + c, p.y_f32) : 0.0f;
+          }
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const int64_t m = m1 + q * kRows;
+            if (m >= p.M) break;
+            const uint32_t at = lds + ((r0 + q * kRows) * kOutStride + c) * 4;
+            if constexpr (kGated)
+              finish_gated1(p, m, n0 + c, *lds_ptr<const float>(at), *lds_ptr<const float>(at + HN * 4));
+            else
+              finish_linear1(p, m, n0 + c, *lds_ptr<const float>(at), res[q]);
+          }
         }
       }
     }
@@ -691,52 +686,80 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_ring_kernel(TileArgs args)
 }
 
 // Sum of the splits' partial results in order, then the epilogue: 8 columns
-// of a row per thread.
+// of a row per thread, four splits' loads in flight.
+constexpr int kJoinThreads = 64;
 template <DenseEpi EPI>
-__global__ __launch_bounds__(256) void join_splits_kernel(TileArgs t) {
+__global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(TileArgs t) {
   const DenseGemm& p = t.p;
   const int64_t runs = (p.N + 7) / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
   if (i >= p.M * runs) return;
   const int64_t m = i / runs, n = i % runs * 8;
-  auto sum = [&](int64_t at, float* v) {
+  constexpr int kKinds = EPI == DenseEpi::kGated ? 2 : 1;
+  float v[kKinds][8] = {};
+  for (int s = 0; s < t.splits; s += 4) {
+    float o[4][kKinds][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    const float* q = t.partial + m * t.ldp + at;
-    for (int s = 0; s < t.splits; ++s, q += p.M * t.ldp) {
-      float o[8];
-      load8(q, 0, true, true, 8, o);
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += o[e];
+      for (int k = 0; k < kKinds; ++k)
+        if (s + q < t.splits) load8(t.partial + ((s + q) * p.M + m) * t.ldp + k * runs * 8, n, true, o[q][k]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (s + q < t.splits) {
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] += o[q][k][e];
+      }
+  }
+  if (t.vec) {
+    if constexpr (EPI == DenseEpi::kGated) {
+      finish_gated(p, m, n, v[0], v[1]);
+    } else {
+      float bias[8];
+      load_bias(p, n, bias);
+      finish_linear(p, m, n, v[0], bias);
     }
-  };
-  float v[8];
-  sum(n, v);
-  if constexpr (EPI == DenseEpi::kGated) {
-    float u[8];
-    sum(runs * 8 + n, u);
-    finish_gated(p, t.vec, m, n, v, u);
   } else {
-    float bias[8];
-    load_bias(p, n, bias);
-    float r[8];
-    if (p.residual) load_residual(p, t.vec, m, n, r);
-    finish_linear(p, t.vec, m, n, v, bias, p.residual != nullptr, r);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      if (n + e >= p.N) break;
+      // v is indexed by constants only
+      float g = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q == e) g = v[0][q], u = v[kKinds - 1][q];
+      if constexpr (EPI == DenseEpi::kGated)
+        finish_gated1(p, m, n + e, g, u);
+      else
+        finish_linear1(p, m, n + e, g, p.residual ? load1(p.residual, m * p.ldr + n + e, p.y_f32) : 0.0f);
+    }
   }
 }
 
+// Up to two copies of operands into rows of whole groups of 8:
 // dst [rows][ldd] = src [rows][cols], the row's padding up to ldd zeroed.
-__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t* __restrict__ src, int64_t lds, int64_t rows,
-                                                        int64_t cols, uint16_t* __restrict__ dst, int64_t ldd) {
-  const int64_t segs = ldd / 8, n = rows * segs;
+struct PackArgs {
+  const uint16_t* src[2];
+  uint16_t* dst[2];
+  int64_t lds[2], rows[2], cols[2];
+};
+__global__ __launch_bounds__(256) void pack_rows_kernel(PackArgs a) {
+  const int w = blockIdx.y;
+  const uint16_t* src = w ? a.src[1] : a.src[0];
+  uint16_t* dst = w ? a.dst[1] : a.dst[0];
+  const int64_t lds = w ? a.lds[1] : a.lds[0], rows = w ? a.rows[1] : a.rows[0], cols = w ? a.cols[1] : a.cols[0];
+  const int64_t segs = (cols + 7) / 8, n = rows * segs;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / segs, c = i % segs * 8;
+    const int64_t r = i >> 32 ? i / segs : static_cast<uint32_t>(i) / static_cast<uint32_t>(segs);
+    const int64_t c = (i - r * segs) * 8;
     const uint16_t* q = src + r * lds + c;
     uint32_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? q[e] : 0;
-    *reinterpret_cast<u32x4*>(dst + r * ldd + c) =
+    *reinterpret_cast<u32x4*>(dst + r * segs * 8 + c) =
         u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
   }
 }
@@ -849,13 +872,6 @@ Plan make_plan(const DenseGemm& p) {
   return pl;
 }
 
-hipError_t pack(const Operand& o, int64_t rows, int64_t cols, uint16_t* dst, hipStream_t s) {
-  const int64_t n = rows * (up8(cols) / 8), blocks = (n + 255) / 256;
-  pack_rows_kernel<<<static_cast<uint32_t>(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(o.p, o.ld, rows, cols, dst,
-                                                                                     up8(cols));
-  return hipGetLastError();
-}
-
 template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
 hipError_t launch_kernel(const TileArgs& t, hipStream_t s) {
   const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(t.tiles_m) * t.tiles_n * t.splits);
@@ -909,15 +925,20 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   TileArgs t{};
   t.p = p;
   hipError_t e = hipSuccess;
-  if (pl.pack_a) {
-    uint16_t* d = reinterpret_cast<uint16_t*>(ws);
-    if ((e = pack(p.a, pl.a_rows, pl.a_cols, d, s)) != hipSuccess) return e;
-    t.p.a = Operand{d, up8(pl.a_cols), p.a.k_rows, true};
-  }
-  if (pl.pack_b) {
-    uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.a_bytes);
-    if ((e = pack(p.b, pl.b_rows, pl.b_cols, d, s)) != hipSuccess) return e;
-    t.p.b = Operand{d, up8(pl.b_cols), p.b.k_rows, true};
+  PackArgs pk{};
+  int packs = 0;
+  auto pack = [&](Operand& o, size_t at, int64_t rows, int64_t cols) {
+    pk.src[packs] = o.p, pk.lds[packs] = o.ld, pk.rows[packs] = rows, pk.cols[packs] = cols;
+    pk.dst[packs] = reinterpret_cast<uint16_t*>(ws + at);
+    o = Operand{pk.dst[packs++], up8(cols), o.k_rows, true};
+  };
+  if (pl.pack_a) pack(t.p.a, 0, pl.a_rows, pl.a_cols);
+  if (pl.pack_b) pack(t.p.b, pl.a_bytes, pl.b_rows, pl.b_cols);
+  if (packs) {
+    const int64_t n0 = pk.rows[0] * (up8(pk.cols[0]) / 8), n1 = pk.rows[1] * (up8(pk.cols[1]) / 8);
+    const int64_t blocks = ((n0 > n1 ? n0 : n1) + 255) / 256;
+    pack_rows_kernel<<<dim3(static_cast<uint32_t>(blocks < 8192 ? blocks : 8192), packs), 256, 0, s>>>(pk);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const bool gated = p.epi == DenseEpi::kGated;
   // padded rows read as zeros up to a multiple of 8
@@ -926,9 +947,9 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   t.a_r = p.a.k_rows ? up8(p.M) : p.M;
   t.b_r = p.b.k_rows ? up8(p.N) : p.N;
   t.vec = row16(p.y, p.ldy, p.y_f32 ? 4 : 2) && row16(p.residual, p.ldr, p.y_f32 ? 4 : 2) &&
-          row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && (!gated || !p.z || p.N % 8 == 0);
+          row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && p.N % 8 == 0;
   t.splits = pl.splits;
-  t.plain = pl.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec && p.N % 8 == 0;
+  t.plain = pl.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec;
   t.chunks = static_cast<int32_t>(pl.chunks);
   t.tiles_m = static_cast<int32_t>(pl.tiles_m);
   t.tiles_n = static_cast<int32_t>(pl.tiles_n);
@@ -944,11 +965,11 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
     case Shape::k64: e = launch_shape<32, 32, 2, 2, 4>(t, s); break;
   }
   if (e != hipSuccess || pl.splits == 1) return e;
-  const int64_t blocks = (p.M * (up8(p.N) / 8) + 255) / 256;
+  const int64_t blocks = (p.M * (up8(p.N) / 8) + kJoinThreads - 1) / kJoinThreads;
   if (gated)
-    join_splits_kernel<DenseEpi::kGated><<<static_cast<uint32_t>(blocks), 256, 0, s>>>(t);
+    join_splits_kernel<DenseEpi::kGated><<<static_cast<uint32_t>(blocks), kJoinThreads, 0, s>>>(t);
   else
-    join_splits_kernel<DenseEpi::kLinear><<<static_cast<uint32_t>(blocks), 256, 0, s>>>(t);
+    join_splits_kernel<DenseEpi::kLinear><<<static_cast<uint32_t>(blocks), kJoinThreads, 0, s>>>(t);
   return hipGetLastError();
 }
 

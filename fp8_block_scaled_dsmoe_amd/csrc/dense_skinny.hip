@@ -13,9 +13,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "act.h"
 #include "common.h"
 #include "dense.h"
+#include "dense_epi.h"
 
 namespace dsmoe {
 namespace {
@@ -23,16 +23,6 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ float load1(const void* p, int64_t i, bool f32) {
-  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
-__device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float v) {
-  if (f32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(f32x2_to_bf16x2(v, 0.0f));
-}
 
 // 8 values from q; VEC: one 16-byte load
 template <bool VEC>
@@ -158,21 +148,10 @@ __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) 
     const int c = i % kCols, m = i / kCols % 16, t = i / (16 * kCols);
     const int64_t row = 16 * t + m, n = n0 + c;
     if (row >= p.M || n >= p.N) continue;
-    if constexpr (kGated) {
-      const float g = total(t, m, c), u = total(t, m, c + 8);
-      if (p.z) {
-        store1(p.z, row * p.ldz + n, false, g);
-        store1(p.z, row * p.ldz + p.N + n, false, u);
-      }
-      store1(p.y, row * p.ldy + n, p.y_f32, act_f32(p.act, g) * u);
-    } else {
-      float v = total(t, m, c);
-      if (p.bias) v += load1(p.bias, n, p.bias_f32);
-      if (p.z) store1(p.z, row * p.ldz + n, p.y_f32, v);
-      v = act_f32(p.act, v);
-      if (p.residual) v += load1(p.residual, row * p.ldr + n, p.y_f32);
-      store1(p.y, row * p.ldy + n, p.y_f32, v);
-    }
+    if constexpr (kGated)
+      finish_gated1(p, row, n, total(t, m, c), total(t, m, c + 8));
+    else
+      finish_linear1(p, row, n, total(t, m, c), p.residual ? load1(p.residual, row * p.ldr + n, p.y_f32) : 0.0f);
   }
 }
 

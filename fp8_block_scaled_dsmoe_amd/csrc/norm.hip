@@ -302,13 +302,13 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
 // the block's rows and leave as one partial row per block, summed by
 // sum_partials_kernel in a fixed order (no atomics: equal calls, equal bits).
 // ---------------------------------------------------------------------------
-constexpr int kBwdPer = 2;
+constexpr int kBwdThreads = 512;
 constexpr int64_t kBwdBlocks = 512;   // 2 per CU
-constexpr int bwd_threads(int nt) { return nt > 512 ? nt : 512; }
 
-template <bool F32, bool VEC, int NT>
-__global__ __launch_bounds__(bwd_threads(NT)) void layer_norm_bwd_kernel(NormBwd p, bool gvec) {
-  constexpr int BT = bwd_threads(NT), RG = BT / NT, PER = kBwdPer;
+// PER: slots of 8 columns per thread
+template <bool F32, bool VEC, int NT, int PER>
+__global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, bool gvec) {
+  constexpr int BT = kBwdThreads, RG = BT / NT;
   constexpr int ES = F32 ? 4 : 2;
   using R = Row<F32, VEC, NT>;
   __shared__ float s_red[2][2 * (BT / 64)];
@@ -340,14 +340,16 @@ __global__ __launch_bounds__(bwd_threads(NT)) void layer_norm_bwd_kernel(NormBwd
       if (p.dsum) nd[v] = R::fetch(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols);
     }
   };
+  constexpr bool kAhead = PER <= 2;   // beyond, there are no registers left for it
   int flip = 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * RG;
-  fetch(static_cast<int64_t>(blockIdx.x) * RG + rg);
+  if (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * RG + rg);
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RG; r0 < p.rows; r0 += stride, flip ^= 1) {
     const int64_t row = r0 + rg;
     const bool live = row < p.rows;
     float x[PER][8], dy[PER][8], sums[2] = {0.0f, 0.0f};
     typename R::Raw ds[PER];
+    if (!kAhead) fetch(row);
     const float mean = nmean, rstd = nrstd;
 #pragma unroll
     for (int v = 0; v < PER; ++v) {
@@ -355,7 +357,7 @@ __global__ __launch_bounds__(bwd_threads(NT)) void layer_norm_bwd_kernel(NormBwd
       R::unpack(ny[v], dy[v]);
       ds[v] = nd[v];
     }
-    fetch(row + stride);
+    if (kAhead) fetch(row + stride);
     if (live) {
 #pragma unroll
       for (int v = 0; v < PER; ++v)
@@ -512,16 +514,17 @@ hipError_t sum_partials(const float* partial, int64_t n, int64_t cols, int64_t s
   return hipGetLastError();
 }
 
-// threads per row of the backward; 0: the long-row kernels
+// threads per row of the backward (two slots each; 512 threads also four); 0:
+// the long-row kernels
 int bwd_nt(int64_t cols) {
-  for (int nt = 64; nt <= 1024; nt *= 2)
-    if (cols <= nt * 8 * kBwdPer) return nt;
-  return 0;
+  for (int nt = 64; nt <= kBwdThreads; nt *= 2)
+    if (cols <= nt * 16) return nt;
+  return cols <= kBwdThreads * 32 ? kBwdThreads : 0;
 }
 int64_t bwd_partial_rows(int64_t rows, int64_t cols) {
   const int nt = bwd_nt(cols);
   if (nt == 0) return rows < 64 ? rows : 64;
-  const int64_t rg = bwd_threads(nt) / nt, blocks = (rows + rg - 1) / rg;
+  const int64_t rg = kBwdThreads / nt, blocks = (rows + rg - 1) / rg;
   return blocks < kBwdBlocks ? blocks : kBwdBlocks;
 }
 
@@ -530,13 +533,16 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t s) {
   const bool gv = p.gamma && al16(p.gamma);
   const uint32_t grid = static_cast<uint32_t>(bwd_partial_rows(p.rows, p.cols));
   switch (bwd_nt(p.cols)) {
-#define DSMOE_LNB(NT) \
-  case NT: layer_norm_bwd_kernel<F32, VEC, NT><<<grid, bwd_threads(NT), 0, s>>>(p, gv); break
-    DSMOE_LNB(64);
-    DSMOE_LNB(128);
-    DSMOE_LNB(256);
-    DSMOE_LNB(512);
-    DSMOE_LNB(1024);
+#define DSMOE_LNB(NT, PER) layer_norm_bwd_kernel<F32, VEC, NT, PER><<<grid, kBwdThreads, 0, s>>>(p, gv)
+    case 64: DSMOE_LNB(64, 2); break;
+    case 128: DSMOE_LNB(128, 2); break;
+    case 256: DSMOE_LNB(256, 2); break;
+    case 512:
+      if (p.cols <= 512 * 16)
+        DSMOE_LNB(512, 2);
+      else
+        DSMOE_LNB(512, 4);
+      break;
 #undef DSMOE_LNB
     default:
       if (p.partial) {
