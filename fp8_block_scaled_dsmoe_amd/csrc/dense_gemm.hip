@@ -179,83 +179,89 @@ struct Half {
   }
 };
 
-// Where a wave's copies of one half read: a resource that starts at the
-// half's chunk and ends with the last valid element, moved on by advance().
+// What a wave copies of one half, chunk by chunk: a buffer resource that starts
+// at the half's chunk and ends with its last valid element, and the lane's
+// offsets in it.  advance() is a few scalar instructions while whole chunks
+// are left; the offsets and the range change only from the last one on.
+// (Masking every copy by its k, and a range computed anew per chunk, cost the
+// multiplies of a one-wave-per-SIMD loop 8 to 10 cycles per vector
+// instruction.)
 template <int HR, bool KROWS, int NW>
 struct Source {
   using H = Half<HR, KROWS, NW>;
-  uint64_t base;          // byte address of the half's (row 0, chunk's first k)
-  int64_t step;           // bytes per chunk
-  int64_t range;          // row operand: valid bytes from base; k-row operand: bytes of the valid columns of a row
-  uint32_t ld2;           // row stride in bytes
-  int32_t k_left;         // valid k from base on
+  uint64_t base;                  // byte address of the half's (row 0, chunk's first k)
+  int32_t range;                  // bytes from base that may be read
+  uint32_t ld2;                   // row stride in bytes
+  int32_t k_left;                 // valid k from base on
+  int32_t cols2;                  // k-row operand: bytes of a row's valid columns
+  int32_t lane_k;                 // row operand: first k of the lane's segment
+  uint32_t voff[H::kCopies];
 
   __device__ __forceinline__ Source() {}
   // rows [r0, r0 + HR) of the operand, chunks from k0 on, k_end: end of valid k
-  __device__ __forceinline__ Source(const Operand& o, int64_t r0, int64_t rows, int64_t k0, int64_t k_end) {
+  __device__ __forceinline__ Source(const Operand& o, int64_t r0, int64_t rows, int64_t k0, int64_t k_end, int wave,
+                                    int lane) {
     ld2 = static_cast<uint32_t>(o.ld * 2);
     const int64_t left = min(static_cast<int64_t>(HR), rows - r0);
-    k_left = static_cast<int32_t>(k_end - k0);
+    k_left = left > 0 ? static_cast<int32_t>(k_end - k0) : 0;
+    lane_k = 8 * ((lane & 7) ^ (lane >> 3));
     if constexpr (KROWS) {
       base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(k0 * o.ld + r0) * 2;
-      step = static_cast<int64_t>(ld2) * kChunk;
-      range = left > 0 ? left * 2 : 0;
+      cols2 = left > 0 ? static_cast<int32_t>(left) * 2 : 0;
+      range = (kChunk - 1) * static_cast<int32_t>(ld2) + cols2;
     } else {
       base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(r0 * o.ld + k0) * 2;
-      step = kChunk * 2;
-      range = left > 0 ? (left - 1) * static_cast<int64_t>(ld2) + 2 * static_cast<int64_t>(k_left) : 0;
+      range = left > 0 ? static_cast<int32_t>(left - 1) * static_cast<int32_t>(ld2) + 2 * k_left : 0;
     }
-    if (left <= 0) k_left = 0;
-  }
-  __device__ __forceinline__ i32x4 resource() const {
-    int64_t n = 0;
-    if (k_left > 0) {
-      if constexpr (KROWS)
-        n = static_cast<int64_t>(min(k_left, kChunk) - 1) * ld2 + range;
-      else
-        n = range;
-    }
-    i32x4 r;
-    r.x = __builtin_amdgcn_readfirstlane(static_cast<int>(base & 0xffffffffu));
-    r.y = __builtin_amdgcn_readfirstlane(static_cast<int>((base >> 32) & 0xffffu));   // raw buffer: stride 0
-    r.z = __builtin_amdgcn_readfirstlane(static_cast<int>(n));
-    r.w = 0x00020000;
-    return r;
-  }
-  // Issue this wave's i-th copy of the current chunk to the half at lds.
-  // rs: resource(); voff: the lane's offsets (lane_offsets); lane_k: the first
-  // k of its segment (row operand).
-  __device__ __forceinline__ void copy(const i32x4& rs, int i, const uint32_t (&voff)[H::kCopies], int lane_k,
-                                       uint32_t lds, int wave) const {
-    // a segment past the row's last valid k would read the next row
-    const uint32_t v = KROWS || lane_k < k_left ? voff[i] : 0x80000000u;
-    copy16(rs, v, __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
-  }
-  __device__ __forceinline__ void advance() {
-    base += step;
-    if constexpr (!KROWS) range -= 2 * kChunk;
-    k_left -= kChunk;
-  }
-  __device__ __forceinline__ void copy_all(const uint32_t (&voff)[H::kCopies], int lane_k, uint32_t lds, int wave) {
-    const i32x4 rs = resource();
-#pragma unroll
-    for (int i = 0; i < H::kCopies; ++i) copy(rs, i, voff, lane_k, lds, wave);
-    advance();
-  }
-  // The lane's byte offsets from base; cols_left: valid columns (k-row operand).
-  static __device__ __forceinline__ void lane_offsets(uint32_t (&voff)[H::kCopies], uint32_t ld2, int64_t cols_left,
-                                                      int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < H::kCopies; ++i) {
       const int j = wave * H::kCopies + i;
       if constexpr (KROWS) {
         const int k = j * H::kRows + lane / H::kSegs, seg = lane % H::kSegs;
         const int col = ((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8;
-        voff[i] = col < cols_left ? static_cast<uint32_t>(k) * ld2 + col * 2 : 0x80000000u;
+        voff[i] = col < left ? static_cast<uint32_t>(k) * ld2 + col * 2 : kOutside;
       } else {
-        voff[i] = static_cast<uint32_t>(8 * j + lane / 8) * ld2 + (((lane & 7) ^ (lane >> 3)) << 4);
+        voff[i] = static_cast<uint32_t>(8 * j + lane / 8) * ld2 + 2 * lane_k;
       }
     }
+    if (k_left < kChunk) cut();
+  }
+  // past every range (the largest is 128 rows of 2^23 bytes)
+  static constexpr uint32_t kOutside = 0x80000000u;
+  // The last chunk, and those past the end: what is past k_left reads as zero.
+  __device__ __forceinline__ void cut() {
+    asm volatile("");   // a branch around it, not selects in every chunk
+    if constexpr (KROWS) {
+      range = k_left > 0 ? (k_left - 1) * static_cast<int32_t>(ld2) + cols2 : 0;
+    } else {
+      if (k_left <= 0) range = 0;
+#pragma unroll
+      for (int i = 0; i < H::kCopies; ++i)
+        if (lane_k >= k_left) voff[i] = kOutside;   // it would read the next row
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (KROWS) {
+      base += ld2 * kChunk;
+    } else {
+      base += 2 * kChunk;
+      range -= 2 * kChunk;   // may pass 0 only where cut() makes it 0
+    }
+    k_left -= kChunk;
+    if (k_left < kChunk) cut();
+  }
+  // Issue this wave's copies of the current chunk to the half at lds.
+  __device__ __forceinline__ void copy(uint32_t lds, int wave) const {
+    // wave-uniform: into scalar registers
+    i32x4 r;
+    r.x = __builtin_amdgcn_readfirstlane(static_cast<int>(base & 0xffffffffu));
+    r.y = __builtin_amdgcn_readfirstlane(static_cast<int>(base >> 32));   // below bit 48: stride 0, a raw buffer
+    r.z = __builtin_amdgcn_readfirstlane(range);
+    r.w = 0x00020000;
+#pragma unroll
+    for (int i = 0; i < H::kCopies; ++i)
+      copy16(r, voff[i],
+             __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
   }
 };
 
@@ -278,14 +284,16 @@ struct Reader {
         at[kk] = (row0 + (lane & 15)) * 128 + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
     }
   }
-  __device__ __forceinline__ bf16x8 read(uint32_t half, int i, int kk) const {
+  // half: the half's place in the stage (a constant: it goes into the
+  // instruction's offset)
+  __device__ __forceinline__ bf16x8 read(uint32_t stage, uint32_t half, int i, int kk) const {
     if constexpr (KROWS) {
-      const uint32_t a = half + at[i] + kk * (32 * HR * 2);
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(a));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(a + 4 * HR * 2));
+      DSMOE_LDS char* a = lds_ptr<char>(stage + at[i]) + (half + kk * (32 * HR * 2));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSMOE_LDS s16x4*)a);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSMOE_LDS s16x4*)(a + 4 * HR * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *lds_ptr<const bf16x8>(half + at[kk] + i * 2048);
+      return *(DSMOE_LDS const bf16x8*)(lds_ptr<char>(stage + at[kk]) + (half + i * 2048));
     }
   }
 };
@@ -333,8 +341,6 @@ struct Tile {
   int64_t m0, n0;
   SA a0, a1;
   SB b0, b1;
-  uint32_t va0[LA], va1[LA], vb0[LB], vb1[LB];
-  const int lane_k;        // row operand: the k of the lane's copies
   const Reader<HM, AT, TM> ra;
   const Reader<HN, BT, TN> rb;
   const uint32_t lds;
@@ -346,7 +352,6 @@ struct Tile {
         wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
         wm(wave / WN),
         wn(wave % WN),
-        lane_k(8 * ((lane & 7) ^ (lane >> 3))),
         ra(wm * (HM / WM), lane),
         rb(wn * (HN / WN), lane),
         lds(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(mem))) {
@@ -361,23 +366,19 @@ struct Tile {
     const int64_t k0 = static_cast<int64_t>(c0) * kChunk;
     const int64_t ka = min(t.a_k, static_cast<int64_t>(c1) * kChunk);
     const int64_t kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
-    a0 = SA(p.a, m0, t.a_r, k0, ka);
-    a1 = SA(p.a, m0 + HM, t.a_r, k0, ka);
+    a0 = SA(p.a, m0, t.a_r, k0, ka, wave, lane);
+    a1 = SA(p.a, m0 + HM, t.a_r, k0, ka, wave, lane);
     Operand up = p.b;   // kGated: the up rows are rows N + n of b
     if constexpr (kGated) up.p += p.N * (BT ? 1 : p.b.ld);
-    b0 = SB(p.b, n0, t.b_r, k0, kb);
-    b1 = SB(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb);
-    SA::lane_offsets(va0, a0.ld2, t.a_r - m0, wave, lane);
-    SA::lane_offsets(va1, a1.ld2, t.a_r - m0 - HM, wave, lane);
-    SB::lane_offsets(vb0, b0.ld2, t.b_r - n0, wave, lane);
-    SB::lane_offsets(vb1, b1.ld2, t.b_r - n0 - (kGated ? 0 : HN), wave, lane);
+    b0 = SB(p.b, n0, t.b_r, k0, kb, wave, lane);
+    b1 = SB(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb, wave, lane);
   }
 
   // the wave's copies of the next chunk of a half into a stage
-  __device__ __forceinline__ void copy_a0(uint32_t stage) { a0.copy_all(va0, lane_k, stage + kA0, wave); }
-  __device__ __forceinline__ void copy_a1(uint32_t stage) { a1.copy_all(va1, lane_k, stage + kA1, wave); }
-  __device__ __forceinline__ void copy_b0(uint32_t stage) { b0.copy_all(vb0, lane_k, stage + kB0, wave); }
-  __device__ __forceinline__ void copy_b1(uint32_t stage) { b1.copy_all(vb1, lane_k, stage + kB1, wave); }
+  __device__ __forceinline__ void copy_a0(uint32_t stage) { a0.copy(stage + kA0, wave), a0.advance(); }
+  __device__ __forceinline__ void copy_a1(uint32_t stage) { a1.copy(stage + kA1, wave), a1.advance(); }
+  __device__ __forceinline__ void copy_b0(uint32_t stage) { b0.copy(stage + kB0, wave), b0.advance(); }
+  __device__ __forceinline__ void copy_b1(uint32_t stage) { b1.copy(stage + kB1, wave), b1.advance(); }
 
   static __device__ __forceinline__ void clear(Acc& acc) {
 #pragma unroll
@@ -564,12 +565,12 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
   w.copy_b1(s1);
   wait_copies<2 * LA + 2 * LB>();   // this wave's part of B0, A0 and B1 of the first chunk
   block_barrier();
-#define DSMOE_READ_A(from)                                        \
+#define DSMOE_READ_A(stage, half)                                        \
   _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = w.ra.read(from, i, kk)
-#define DSMOE_READ_B(f, from)                                     \
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = w.ra.read(stage, half, i, kk)
+#define DSMOE_READ_B(f, stage, half)                                     \
   _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = w.rb.read(from, j, kk)
+      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = w.rb.read(stage, half, j, kk)
   // The end of a phase's reads and copies: the reads are done (the halves may
   // be refilled once all waves are past the barrier), and what the next phase
   // reads is there (at most the copies of this phase and the last may still be
@@ -591,7 +592,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
     __builtin_amdgcn_sched_barrier(0);                                                                           \
     block_barrier();                                                                    \
   } while (0)
-  DSMOE_READ_B(0, s0 + T::kB0);
+  DSMOE_READ_B(0, s0, T::kB0);
   wait_lds();
   block_barrier();
   if (w.wm == 1) block_barrier();
@@ -600,14 +601,14 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
   // reads; it has registers of its own and moves at the end.
   uint32_t st = s0, nx = s1;
   for (int32_t c = w.c0; c < w.c1; ++c) {
-    DSMOE_READ_A(st + T::kA0);
-    DSMOE_READ_B(1, st + T::kB1);
+    DSMOE_READ_A(st, T::kA0);
+    DSMOE_READ_B(1, st, T::kB1);
     __builtin_amdgcn_sched_barrier(0);
     w.copy_a1(nx);
     w.copy_b0(st);
     DSMOE_PHASE(0);
-    DSMOE_READ_A(st + T::kA1);
-    DSMOE_READ_B(2, nx + T::kB0);
+    DSMOE_READ_A(st, T::kA1);
+    DSMOE_READ_B(2, nx, T::kB0);
     __builtin_amdgcn_sched_barrier(0);
     w.copy_a0(st);
     w.copy_b1(st);
@@ -647,9 +648,9 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_ring_kernel(TileArgs args)
   do {                                                                                                     \
     _Pragma("unroll") for (int h = 0; h < 2; ++h) {                                                        \
       _Pragma("unroll") for (int i = 0; i < TM; ++i) fa[kk][h][i] =                                        \
-          w.ra.read((stage) + (h ? T::kA1 : T::kA0), i, kk);                                               \
+          w.ra.read(stage, h ? T::kA1 : T::kA0, i, kk);                                               \
       _Pragma("unroll") for (int j = 0; j < TN; ++j) fb[kk][h][j] =                                        \
-          w.rb.read((stage) + (h ? T::kB1 : T::kB0), j, kk);                                               \
+          w.rb.read(stage, h ? T::kB1 : T::kB0, j, kk);                                               \
     }                                                                                                      \
   } while (0)
 #define DSMOE_PRODUCTS(kk)                                                                                 \
