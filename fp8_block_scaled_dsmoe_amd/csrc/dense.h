@@ -74,6 +74,7 @@ enum class DenseEpi : int {
 struct DenseGemm {
   Operand a, b;           // a: M rows, b: N rows (kGated: 2 N rows, gate rows first)
   int64_t M, N, K;
+  int64_t gate_n;         // kGated: rows of b (columns of z) from a gate to its up row: N of the whole product
   DenseEpi epi;
   int act;
   const void* bias;       // [N] or null

@@ -55,7 +55,7 @@ DenseGemm forward_product(const void* x, int64_t ldx, const void* w, int64_t ldw
   DenseGemm g{};
   g.a = operand(x, ldx, false);
   g.b = operand(w, ldw, false);
-  g.M = M, g.N = N, g.K = K, g.epi = epi;
+  g.M = M, g.N = N, g.K = K, g.gate_n = N, g.epi = epi;
   return g;
 }
 // dx [M][K] = dz [M][N] w [N][K]

@@ -33,7 +33,7 @@ __device__ __forceinline__ void finish_linear1(const DenseGemm& p, int64_t m, in
 __device__ __forceinline__ void finish_gated1(const DenseGemm& p, int64_t m, int64_t n, float g, float u) {
   if (p.z) {
     store1(p.z, m * p.ldz + n, false, g);
-    store1(p.z, m * p.ldz + p.N + n, false, u);
+    store1(p.z, m * p.ldz + p.gate_n + n, false, u);
   }
   store1(p.y, m * p.ldy + n, p.y_f32, act_f32(p.act, g) * u);
 }

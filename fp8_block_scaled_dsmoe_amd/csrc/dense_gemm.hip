@@ -116,7 +116,7 @@ __device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int
 __device__ __forceinline__ void finish_gated(const DenseGemm& p, int64_t m, int64_t n, const float* g, const float* u) {
   if (p.z) {
     store8(p.z, m * p.ldz + n, false, g);
-    store8(p.z, m * p.ldz + p.N + n, false, u);
+    store8(p.z, m * p.ldz + p.gate_n + n, false, u);
   }
   float v[8];
 #pragma unroll
@@ -167,10 +167,12 @@ __device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "
 template <int HR, bool KROWS, int NW>
 struct Half {
   static constexpr int kBytes = HR * 128;
-  static constexpr int kCopies = HR / (8 * NW);       // copies per wave and half
-  static_assert(HR % (8 * NW) == 0, "whole copies");
-  static constexpr int kSegs = HR / 8;                // k-row operand: 16-byte segments of a row
-  static constexpr int kRows = 64 / kSegs;            // rows of k per copy
+  static constexpr int kAll = HR / 8;                      // copies of 1 KB
+  static constexpr int kCopies = (kAll + NW - 1) / NW;     // of a wave
+  static constexpr int kSegs = HR / 8;                     // k-row operand: 16-byte segments of a row
+  // the wave's i-th copy; where they do not come out even the last one is
+  // made more than once (the same bytes to the same place)
+  static __device__ __forceinline__ int index(int wave, int i) { return min(wave * kCopies + i, kAll - 1); }
 
   static __device__ __forceinline__ int key(int k) {
     if constexpr (HR == 128) return (k & 3) | ((k >> 3) & 1) << 2;
@@ -215,9 +217,9 @@ struct Source {
     }
 #pragma unroll
     for (int i = 0; i < H::kCopies; ++i) {
-      const int j = wave * H::kCopies + i;
+      const int j = H::index(wave, i);
       if constexpr (KROWS) {
-        const int k = j * H::kRows + lane / H::kSegs, seg = lane % H::kSegs;
+        const int k = (j * 64 + lane) / H::kSegs, seg = (j * 64 + lane) % H::kSegs;
         const int col = ((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8;
         voff[i] = col < left ? static_cast<uint32_t>(k) * ld2 + col * 2 : kOutside;
       } else {
@@ -261,7 +263,7 @@ struct Source {
 #pragma unroll
     for (int i = 0; i < H::kCopies; ++i)
       copy16(r, voff[i],
-             __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(wave * H::kCopies + i) * 1024));
+             __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(H::index(wave, i)) * 1024));
   }
 };
 
@@ -368,8 +370,8 @@ struct Tile {
     const int64_t kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
     a0 = SA(p.a, m0, t.a_r, k0, ka, wave, lane);
     a1 = SA(p.a, m0 + HM, t.a_r, k0, ka, wave, lane);
-    Operand up = p.b;   // kGated: the up rows are rows N + n of b
-    if constexpr (kGated) up.p += p.N * (BT ? 1 : p.b.ld);
+    Operand up = p.b;   // kGated: the up rows are rows gate_n + n of b
+    if constexpr (kGated) up.p += p.gate_n * p.b.ld;
     b0 = SB(p.b, n0, t.b_r, k0, kb, wave, lane);
     b1 = SB(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb, wave, lane);
   }
@@ -392,8 +394,14 @@ struct Tile {
   // The results pass through LDS, half of the tile's rows at a time, so that a
   // thread finishes runs of 8 columns and a wave writes whole lines.
   static constexpr int kRuns = (kGated ? HN : 2 * HN) / 8;   // of 8 columns
-  static constexpr int kRowsAtOnce = 64 * NW / kRuns < HM ? 64 * NW / kRuns : HM;
-  static_assert(64 * NW % kRuns == 0 && HM % kRowsAtOnce == 0, "whole rows");
+  // rows that the block's threads take at once, a power of 2 (with 24 runs a
+  // quarter of the threads stay out)
+  static constexpr int rows_at_once(int per_row) {
+    int r = 1;
+    while (2 * r * per_row <= 64 * NW && 2 * r <= HM) r *= 2;
+    return r;
+  }
+  static constexpr int kRowsAtOnce = rows_at_once(kRuns);
 
   // Half ha of the results to LDS.  A result lane holds row l % 16 of its A
   // fragment and columns 4 (l / 16) + [0, 4) of its B fragment; rows 16 bytes
@@ -430,7 +438,7 @@ struct Tile {
     constexpr int R = HM / kRowsAtOnce, Q = F32 ? 2 : 1, ES = F32 ? 4 : 2;
     const int run = threadIdx.x % kRuns, r0 = threadIdx.x / kRuns;
     const int64_t n = n0 + run * 8;
-    const bool in = n < p.N && r0 < HM;
+    const bool in = n < p.N && r0 < kRowsAtOnce;
     float bias[8];
     load_bias(p, n, bias);
     u32x4 res[2][R][Q];
@@ -495,6 +503,7 @@ struct Tile {
     for (int ha = 0; ha < 2; ++ha) {
       put(acc[ha]);
       if (runs) {
+        if (static_cast<int>(threadIdx.x) >= kRowsAtOnce * kRuns) continue;
 #pragma unroll 1
         for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
           const int64_t m = m0 + ha * HM + r;
@@ -514,10 +523,10 @@ struct Tile {
       } else {
         // rows of no alignment: one column per thread, adjacent lanes adjacent
         // columns, the residuals of kBatch rows loaded first
-        constexpr int kCols = kRuns * 8, kRows = 64 * NW / kCols, kBatch = HM / kRows < 4 ? HM / kRows : 4;
-        static_assert(64 * NW % kCols == 0 && HM % (kRows * kBatch) == 0, "whole batches");
+        constexpr int kCols = kRuns * 8, kRows = rows_at_once(kCols), kBatch = HM / kRows < 4 ? HM / kRows : 4;
+        static_assert(HM % (kRows * kBatch) == 0, "whole batches");
         const int c = threadIdx.x % kCols;
-        if (n0 + c >= p.N) continue;
+        if (n0 + c >= p.N || static_cast<int>(threadIdx.x) >= kRows * kCols) continue;
 #pragma unroll 1
         for (int r0 = threadIdx.x / kCols; r0 < HM; r0 += kRows * kBatch) {
           const int64_t m1 = m0 + ha * HM + r0;
@@ -543,7 +552,8 @@ struct Tile {
   }
 };
 
-// The 256 x 256 tile: two stages of LDS refilled half by half.
+// The 256-row tiles: two stages of LDS refilled half by half.  Waves w and w + 4
+// share a SIMD.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
@@ -595,7 +605,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
   DSMOE_READ_B(0, s0, T::kB0);
   wait_lds();
   block_barrier();
-  if (w.wm == 1) block_barrier();
+  if (w.wave >= 4) block_barrier();
 
   // The next chunk's B0 is read in the second phase, to even out the phases'
   // reads; it has registers of its own and moves at the end.
@@ -621,7 +631,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
     st = nx;
     nx = sw;
   }
-  if (w.wm == 0) block_barrier();
+  if (w.wave < 4) block_barrier();
 #undef DSMOE_READ_A
 #undef DSMOE_READ_B
 #undef DSMOE_PHASE
@@ -790,30 +800,38 @@ __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd
 //              (1024 x 4096 x 4096 in 38 us; with two stages 45, 256 x 256 80)
 //   128 x 128  two stages, two per CU: a few tiles per CU and few chunks
 //              (16384 x 512 x 512 in 15.9 us; four stages 19.5, 256 x 256 22.7)
+//   256 x 192  phased: what is left over when 256 x 256 tiles fill the card a
+//              whole number of times (see make_plan), and sizes it fits better
 //   128 x 256  three stages, one per CU: when 256 x 256 leaves CUs without a
 //              tile (4096 x 2048 x 7168 in 103 us; 128 x 128 117, 256 x 256 173)
 //   64 x 64    four stages, two per CU: small products
 //              (1024^3 in 9.5 us; 128 x 128 12.8)
-enum class Shape { k256, k128x256, k128x4, k128x2, k64 };
+enum class Shape { k256, k256x192, k128x256, k128x4, k128x2, k64 };
 struct ShapeInfo {
   int64_t rows, cols;
   int per_cu;
   double chunk_us, shared_us, end_us;
 };
 constexpr ShapeInfo kShapes[] = {
-    {256, 256, 1, 1.50, 0.0, 5.0},  {128, 256, 1, 0.90, 0.0, 4.0}, {128, 128, 1, 0.53, 0.0, 3.0},
-    {128, 128, 2, 0.62, 1.05, 3.0}, {64, 64, 2, 0.30, 0.42, 2.0}};
+    {256, 256, 1, 1.42, 0.0, 5.0}, {256, 192, 1, 1.12, 0.0, 4.5},  {128, 256, 1, 0.88, 0.0, 4.0},
+    {128, 128, 1, 0.50, 0.0, 3.0}, {128, 128, 2, 0.60, 1.00, 3.0}, {64, 64, 2, 0.30, 0.42, 2.0}};
 constexpr int64_t kCus = 256;
 constexpr double kHbm = 4.8e6;   // bytes per us of a long read
 
-struct Plan {
+struct Grid {   // a launch of dense_*_kernel
   Shape shape;
   int splits;
-  int64_t tiles_m, tiles_n, chunks;
+  int64_t tiles_m, tiles_n;
+  double us;    // estimated time
+};
+struct Plan {
+  Grid first, rest;
+  int64_t cut;    // columns of the result in the first launch; 0: all, there is no other
+  int64_t chunks;
   bool pack_a, pack_b;
   int64_t a_rows, a_cols, b_rows, b_cols;   // of the stored matrices
   size_t a_bytes, b_bytes, partial_bytes;
-  double us;   // estimated time
+  double us;      // estimated time
 };
 
 bool row16(const void* p, int64_t ld, int es) {
@@ -836,6 +854,24 @@ double blocks_us(const ShapeInfo& s, int64_t n, int64_t chunks) {
   return static_cast<double>(n / slots) * full + (rest == 0 ? 0.0 : rest <= kCus ? alone : full);
 }
 
+// Shape and number of splits of K for m rows and nb rows of b by the estimated
+// time: the blocks, and with splits the launch that joins them and the partial
+// sums' way to memory and back.
+Grid best_grid(int64_t m, int64_t nb, int64_t chunks, int max_splits) {
+  Grid g{};
+  g.us = 1e30;
+  for (int i = 0; i < 6; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    const int64_t tm = (m + s.rows - 1) / s.rows, tn = (nb + s.cols - 1) / s.cols;
+    for (int sp = 1; sp <= max_splits && sp <= chunks; sp *= 2) {
+      double us = blocks_us(s, tm * tn * sp, (chunks + sp - 1) / sp);
+      if (sp > 1) us += 4.0 + 2.0 * sp * static_cast<double>(m) * nb * 4 / 4e6;
+      if (us < g.us) g = Grid{static_cast<Shape>(i), sp, tm, tn, us};
+    }
+  }
+  return g;
+}
+
 Plan make_plan(const DenseGemm& p) {
   Plan pl{};
   const bool gated = p.epi == DenseEpi::kGated;
@@ -848,28 +884,32 @@ Plan make_plan(const DenseGemm& p) {
   pl.b_bytes = pl.pack_b ? up256(static_cast<size_t>(pl.b_rows) * up8(pl.b_cols) * 2) : 0;
   pl.chunks = (p.K + kChunk - 1) / kChunk;
 
-  // Shape and number of splits of K by the estimated time: the blocks, and
-  // with splits the launch that joins them and the partial sums' way to memory
-  // and back.
-  double best = 1e30;
-  for (int i = 0; i < 5; ++i) {
-    const ShapeInfo& s = kShapes[i];
-    const int64_t tm = (p.M + s.rows - 1) / s.rows, tn = (nb + s.cols - 1) / s.cols;
-    for (int sp = 1; sp <= 32 && sp <= pl.chunks; sp *= 2) {
-      double us = blocks_us(s, tm * tn * sp, (pl.chunks + sp - 1) / sp);
-      if (sp > 1) us += 4.0 + 2.0 * sp * static_cast<double>(p.M) * nb * 4 / 4e6;
-      if (us < best) {
-        best = us;
-        pl.shape = static_cast<Shape>(i), pl.splits = sp, pl.tiles_m = tm, pl.tiles_n = tn;
-      }
+  pl.first = best_grid(p.M, nb, pl.chunks, 32);
+  // Tiles of 256 x 256 that fill the card a whole number of times, and another
+  // launch for the columns left over: 4096 x 7168 is one round of 256 such
+  // tiles and one of 256 tiles of 256 x 192, instead of two rounds of which
+  // the second has 192.
+  const ShapeInfo& big = kShapes[static_cast<int>(Shape::k256)];
+  const int64_t tm = (p.M + big.rows - 1) / big.rows, tn = (nb + big.cols - 1) / big.cols;
+  for (int64_t rounds = 1; rounds * kCus < tm * tn && rounds <= 8; ++rounds) {
+    const int64_t c = rounds * kCus / tm;   // tile columns of the first launch
+    if (c < 1 || c >= tn) continue;
+    const Grid rest = best_grid(p.M, nb - c * big.cols, pl.chunks, 1);
+    const double first_us = blocks_us(big, tm * c, pl.chunks), us = first_us + rest.us + 3.0;
+    if (us < pl.first.us + (pl.cut ? pl.rest.us + 3.0 : 0.0)) {
+      pl.cut = c * (gated ? big.cols / 2 : big.cols);
+      pl.first = Grid{Shape::k256, 1, tm, c, first_us};
+      pl.rest = rest;
     }
   }
+  const double work = pl.first.us + (pl.cut ? pl.rest.us + 3.0 : 0.0);
   // launches, W's way from memory, copies of operands
   const double bytes = static_cast<double>(nb) * p.K * 2;
-  pl.us = 3.5 + (best > bytes / kHbm ? best + 0.25 * bytes / kHbm : bytes / kHbm + 0.25 * best);
+  pl.us = 3.5 + (work > bytes / kHbm ? work + 0.25 * bytes / kHbm : bytes / kHbm + 0.25 * work);
   if (pl.pack_a) pl.us += 3.0 + 2.0 * pl.a_bytes / kHbm;
   if (pl.pack_b) pl.us += 3.0 + 2.0 * pl.b_bytes / kHbm;
-  pl.partial_bytes = pl.splits > 1 ? static_cast<size_t>(pl.splits) * p.M * (gated ? 2 * up8(p.N) : up8(p.N)) * 4 : 0;
+  if (pl.first.splits > 1)
+    pl.partial_bytes = static_cast<size_t>(pl.first.splits) * p.M * (gated ? 2 * up8(p.N) : up8(p.N)) * 4;
   return pl;
 }
 
@@ -877,7 +917,7 @@ template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
 hipError_t launch_kernel(const TileArgs& t, hipStream_t s) {
   const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(t.tiles_m) * t.tiles_n * t.splits);
   constexpr int threads = 64 * WM * WN;
-  if constexpr (HM == 128 && HN == 128)
+  if constexpr (HM == 128)
     dense_phased_kernel<HM, HN, WM, WN, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   else
     dense_ring_kernel<HM, HN, WM, WN, S, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
@@ -949,23 +989,47 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   t.b_r = p.b.k_rows ? up8(p.N) : p.N;
   t.vec = row16(p.y, p.ldy, p.y_f32 ? 4 : 2) && row16(p.residual, p.ldr, p.y_f32 ? 4 : 2) &&
           row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && p.N % 8 == 0;
-  t.splits = pl.splits;
-  t.plain = pl.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec;
   t.chunks = static_cast<int32_t>(pl.chunks);
-  t.tiles_m = static_cast<int32_t>(pl.tiles_m);
-  t.tiles_n = static_cast<int32_t>(pl.tiles_n);
-  if (pl.splits > 1) {
+  auto run = [&](const Grid& g) {
+    t.splits = g.splits;
+    t.plain = g.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec;
+    t.tiles_m = static_cast<int32_t>(g.tiles_m);
+    t.tiles_n = static_cast<int32_t>(g.tiles_n);
+    switch (g.shape) {
+      case Shape::k256: return launch_shape<128, 128, 2, 4, 2>(t, s);
+      case Shape::k256x192: return launch_shape<128, 96, 4, 2, 2>(t, s);
+      case Shape::k128x256: return launch_shape<64, 128, 2, 4, 3>(t, s);
+      case Shape::k128x4: return launch_shape<64, 64, 2, 4, 4>(t, s);
+      case Shape::k128x2: return launch_shape<64, 64, 2, 4, 2>(t, s);
+      case Shape::k64: break;
+    }
+    return launch_shape<32, 32, 2, 2, 4>(t, s);
+  };
+  if (pl.cut) {
+    DenseGemm& q = t.p;
+    q.N = pl.cut;
+    t.b_r = q.b.k_rows ? up8(q.N) : q.N;
+    if ((e = run(pl.first)) != hipSuccess) return e;
+    // the columns from cut on
+    q.N = p.N - pl.cut;
+    t.b_r = q.b.k_rows ? up8(q.N) : q.N;
+    q.b.p += q.b.k_rows ? pl.cut : pl.cut * q.b.ld;
+    const int64_t es = q.y_f32 ? 4 : 2;
+    auto move = [&](const void* m, int64_t size) {
+      return m ? static_cast<const void*>(static_cast<const char*>(m) + pl.cut * size) : nullptr;
+    };
+    q.y = const_cast<void*>(move(q.y, es));
+    q.residual = move(q.residual, es);
+    q.bias = move(q.bias, q.bias_f32 ? 4 : 2);
+    q.z = const_cast<void*>(move(q.z, gated ? 2 : es));
+    return run(pl.rest);
+  }
+  if (pl.first.splits > 1) {
     t.partial = reinterpret_cast<float*>(ws + pl.a_bytes + pl.b_bytes);
     t.ldp = gated ? 2 * up8(p.N) : up8(p.N);
   }
-  switch (pl.shape) {
-    case Shape::k256: e = launch_shape<128, 128, 2, 4, 2>(t, s); break;
-    case Shape::k128x256: e = launch_shape<64, 128, 2, 4, 3>(t, s); break;
-    case Shape::k128x4: e = launch_shape<64, 64, 2, 4, 4>(t, s); break;
-    case Shape::k128x2: e = launch_shape<64, 64, 2, 4, 2>(t, s); break;
-    case Shape::k64: e = launch_shape<32, 32, 2, 2, 4>(t, s); break;
-  }
-  if (e != hipSuccess || pl.splits == 1) return e;
+  e = run(pl.first);
+  if (e != hipSuccess || pl.first.splits == 1) return e;
   const int64_t blocks = (p.M * (up8(p.N) / 8) + kJoinThreads - 1) / kJoinThreads;
   if (gated)
     join_splits_kernel<DenseEpi::kGated><<<static_cast<uint32_t>(blocks), kJoinThreads, 0, s>>>(t);

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) 
   int64_t wrow;
   if constexpr (kGated) {
     const int64_t n = min(n0 + (r & 7), p.N - 1);
-    wrow = r < 8 ? n : p.N + n;
+    wrow = r < 8 ? n : p.gate_n + n;
   } else {
     wrow = min(n0 + r, p.N - 1);
   }

@@ -541,3 +541,52 @@ def test_dense_ffn_step(d):
         num = (loss(**up) - loss(**lo)) / 2e-5
         terms = host(got[key]).astype(np.float64) * v
         assert abs(terms.sum() - num) <= 8 * 5 * V * np.linalg.norm(terms), (key, terms.sum(), num)
+
+
+@pytest.mark.parametrize("M,I,H", [(4104, 2180, 1096), (2048, 5000, 600), (4096, 2048, 1032)])
+def test_gated_linear_large(d, M, I, H):
+    """Sizes of several tile shapes in one product, checked on sampled rows and
+    columns (of the gate and the matching up half)."""
+    banner(f"gated_linear {M}x{I}x{H}")
+    g = torch.Generator(device="cuda").manual_seed(M + I)
+    x = torch.randn((M, H), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((2 * I, H), generator=g, device="cuda") * 0.05).bfloat16()
+    hs = torch.randn((M, 2 * I), generator=g, device="cuda").bfloat16()
+    da = (torch.randn((M, I), generator=g, device="cuda") * 0.1).bfloat16()
+    a, h = d.gated_linear(x, w, "gelu", torch.float32, save_h=True)
+    dx, dw = d.gated_linear_backward(da, x, w, hs, "silu", torch.float32, torch.float32)
+    r = np.random.default_rng(1)
+    rm = np.unique(np.r_[0, M - 1, r.integers(0, M, 40)])
+    ri = np.unique(np.r_[0, I - 1, r.integers(0, I, 40)])
+    rh = np.unique(np.r_[0, H - 1, r.integers(0, H, 40)])
+    both = np.r_[ri, I + ri]
+    x64, w64, hs64, da64 = (host(t).astype(np.float64) for t in (x, w, hs, da))
+    _gated_check(a[rm], h[rm], x64[rm], w64, "gelu", "f32", "rows")
+    _gated_check(a[:, ri], h[:, both], x64, w64[both], "gelu", "f32", "columns")
+    _, _, dh = od.gated_linear_backward(da64, x64, w64, hs64)
+    rounded = 4 * V + 2.0 ** -19
+    for got, p, q, what in ((dx[rm], dh[rm], w64, "dx rows"), (dx[:, rh], dh, w64[:, rh], "dx columns"),
+                            (dw[both], dh[:, both].T, x64, "dw rows"), (dw[:, rh], dh.T, x64[:, rh], "dw columns")):
+        bound = 16 * U * _norms(p, q.T) + rounded * np.sqrt((p * p) @ (q * q))
+        _close(got, p @ q, bound, "f32", what)
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 7168, 520), (4200, 6000, 328), (2100, 9000, 200), (8192, 1544, 264)])
+def test_linear_tile_shapes(d, M, N, K):
+    """Wide results that take more than one round of tiles: residual, bias and
+    pre-activation over the seams between launches and shapes."""
+    banner(f"linear shapes {M}x{N}x{K}")
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((N, K), generator=g, device="cuda") * 0.1).bfloat16()
+    bias = torch.randn((N,), generator=g, device="cuda")
+    r = np.random.default_rng(2)
+    rm = np.unique(np.r_[0, M - 1, r.integers(0, M, 60)])
+    x64, w64, b64 = host(x).astype(np.float64), host(w).astype(np.float64), host(bias).astype(np.float64)
+    for kind, out in (("none", "bf16"), ("silu", "f32")):
+        res = torch.randn((M, N), generator=g, device="cuda").to(DT[out])
+        y, z = d.linear(x, w, bias, kind, res, DT[out], save_z=True)
+        res64 = host(res[rm]).astype(np.float64)
+        _linear_check(y[rm], z[rm], x64[rm], w64, b64, kind, res64, out, f"{kind} {out}")
+        y2, _ = d.linear(x, w, bias, kind, res, DT[out])
+        assert torch.equal(y, y2)
