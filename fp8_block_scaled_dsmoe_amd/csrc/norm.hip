@@ -303,7 +303,9 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
 // sum_partials_kernel in a fixed order (no atomics: equal calls, equal bits).
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
-constexpr int64_t kBwdBlocks = 512;   // 2 per CU
+// One block per CU: its 160 registers leave no room for a second, and every
+// block writes a partial row (512 blocks took 67 us on 4096 x 7168, 256 take 53)
+constexpr int64_t kBwdBlocks = 256;
 
 // PER: slots of 8 columns per thread
 template <bool F32, bool VEC, int NT, int PER>
