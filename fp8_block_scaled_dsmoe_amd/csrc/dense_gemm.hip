@@ -949,17 +949,7 @@ bool few_tokens(const DenseGemm& p, const Plan& pl) {
   return 4.0 + (w > x ? w + 0.3 * x : x + 0.3 * w) < pl.us;
 }
 
-}  // namespace
-
-bool operand_copyable(const Operand& o, int64_t cols) { return copyable(o, cols); }
-
-size_t dense_gemm_workspace_bytes(const DenseGemm& p) {
-  const Plan pl = make_plan(p);
-  if (few_tokens(p, pl)) return 0;
-  return pl.a_bytes + pl.b_bytes + up256(pl.partial_bytes);
-}
-
-hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
+hipError_t launch_range(const DenseGemm& p, hipStream_t s) {
   const Plan pl = make_plan(p);
   if (few_tokens(p, pl)) return launch_dense_skinny(p, s);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
@@ -1036,6 +1026,46 @@ hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   else
     join_splits_kernel<DenseEpi::kLinear><<<static_cast<uint32_t>(blocks), kJoinThreads, 0, s>>>(t);
   return hipGetLastError();
+}
+
+// A launch holds fewer than 2^32 threads: f with ranges of at most 2^28 of the
+// result's rows (2^30 threads in tiles of 64 x 64; wider results take larger
+// tiles).  dW's rows are a dimension of the weights.
+template <typename F>
+hipError_t by_row_ranges(const DenseGemm& p, F f) {
+  constexpr int64_t kRows = int64_t{1} << 28;
+  if (p.a.k_rows || p.M <= kRows) return f(p);
+  const int64_t ys = p.y_f32 ? 4 : 2, zs = p.epi == DenseEpi::kGated ? 2 : ys;
+  for (int64_t r = 0; r < p.M; r += kRows) {
+    DenseGemm q = p;
+    q.M = p.M - r < kRows ? p.M - r : kRows;
+    if (p.a.p) q.a.p += r * p.a.ld;
+    if (p.y) q.y = static_cast<char*>(p.y) + r * p.ldy * ys;
+    if (p.residual) q.residual = static_cast<const char*>(p.residual) + r * p.ldr * ys;
+    if (p.z) q.z = static_cast<char*>(p.z) + r * p.ldz * zs;
+    const hipError_t e = f(q);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+bool operand_copyable(const Operand& o, int64_t cols) { return copyable(o, cols); }
+
+size_t dense_gemm_workspace_bytes(const DenseGemm& p) {
+  size_t most = 0;
+  (void)by_row_ranges(p, [&](const DenseGemm& q) {
+    const Plan pl = make_plan(q);
+    const size_t n = few_tokens(q, pl) ? 0 : pl.a_bytes + pl.b_bytes + up256(pl.partial_bytes);
+    most = n > most ? n : most;
+    return hipSuccess;
+  });
+  return most;
+}
+
+hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
+  return by_row_ranges(p, [&](const DenseGemm& q) { return launch_range(q, s); });
 }
 
 hipError_t launch_zero_matrix(void* dst, int64_t ldd, bool f32, int64_t m, int64_t n, hipStream_t s) {

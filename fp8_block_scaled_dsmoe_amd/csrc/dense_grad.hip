@@ -107,44 +107,47 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
   }
 }
 
-// One slot of 8 columns of da per thread.
+// One slot of 8 columns of da per thread and pass over the grid.
 __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __restrict__ da, int64_t ldda,
                                                              const uint16_t* __restrict__ h, int64_t ldh, bool vec,
                                                              int act, int64_t M, int64_t I,
                                                              uint16_t* __restrict__ dh, int64_t lddh) {
   const uint32_t slots = static_cast<uint32_t>((I + 7) / 8);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= M * slots) return;
-  // 32-bit division where the index allows it
-  const int64_t r = i >> 32 ? i / slots : static_cast<uint32_t>(i) / slots;
-  const int64_t c = 8 * (i - r * slots);
-  float d[8], g[8], u[8], dg[8], du[8];
-  load8<false>(da + r * ldda, c, I, vec, d);
-  load8<false>(h + r * ldh, c, I, vec, g);
-  load8<false>(h + r * ldh + I, c, I, vec, u);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < M * slots;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    // 32-bit division where the index allows it
+    const int64_t r = i >> 32 ? i / slots : static_cast<uint32_t>(i) / slots;
+    const int64_t c = 8 * (i - r * slots);
+    float d[8], g[8], u[8], dg[8], du[8];
+    load8<false>(da + r * ldda, c, I, vec, d);
+    load8<false>(h + r * ldh, c, I, vec, g);
+    load8<false>(h + r * ldh + I, c, I, vec, u);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float f, df;
-    act_and_grad_f32(act, g[e], f, df);
-    dg[e] = d[e] * u[e] * df;
-    du[e] = d[e] * f;
-  }
-  uint16_t* o = dh + r * lddh + c;
-  if (vec) {
-    *reinterpret_cast<u32x4*>(o) = pack8(dg);
-    *reinterpret_cast<u32x4*>(o + I) = pack8(du);
-  } else {
+    for (int e = 0; e < 8; ++e) {
+      float f, df;
+      act_and_grad_f32(act, g[e], f, df);
+      dg[e] = d[e] * u[e] * df;
+      du[e] = d[e] * f;
+    }
+    uint16_t* o = dh + r * lddh + c;
+    if (vec) {
+      *reinterpret_cast<u32x4*>(o) = pack8(dg);
+      *reinterpret_cast<u32x4*>(o + I) = pack8(du);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < I) {
-        o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
-        o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
-      }
-    // the row's padding past 2 I, by the thread that owns the last column
-    if (c + 8 >= I)
-      for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
+      for (int e = 0; e < 8; ++e)
+        if (c + e < I) {
+          o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
+          o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
+        }
+      // the row's padding past 2 I, by the thread that owns the last column
+      if (c + 8 >= I)
+        for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
+    }
   }
 }
+
+constexpr int64_t kMaxBlocks = 1 << 23;   // 2^31 threads; a launch holds fewer than 2^32
 
 bool row16(const void* p, int64_t ld, int es) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
@@ -190,8 +193,9 @@ hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_
                                  int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s) {
   if (M == 0) return hipSuccess;
   const bool vec = I % 8 == 0 && row16(da, ldda, 2) && row16(h, ldh, 2);
-  const int64_t blocks = (M * ((I + 7) / 8) + 255) / 256;
-  gated_backward_kernel<<<static_cast<uint32_t>(blocks), 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, dh, lddh);
+  const int64_t all = (M * ((I + 7) / 8) + 255) / 256;
+  const uint32_t blocks = static_cast<uint32_t>(all < kMaxBlocks ? all : kMaxBlocks);
+  gated_backward_kernel<<<blocks, 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, dh, lddh);
   return hipGetLastError();
 }
 

@@ -167,15 +167,15 @@ constexpr int kFwdThreads = 256;
 
 // One row per NT threads.
 template <bool F32, bool VEC, int NT, int PER>
-__global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_norm_kernel(NormFwd p, bool gvec,
-                                                                                         bool bvec) {
+__global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_norm_kernel(NormFwd p, int64_t row0,
+                                                                                         bool gvec, bool bvec) {
   constexpr int BT = NT > kFwdThreads ? NT : kFwdThreads;
   constexpr int ES = F32 ? 4 : 2;
   using R = Row<F32, VEC, NT>;
   __shared__ float s_red[2][BT / 64];
   const int wave = threadIdx.x >> 6;
   const int t = threadIdx.x % NT;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (BT / NT) + threadIdx.x / NT;
+  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (BT / NT) + threadIdx.x / NT;
   if (NT <= 64 && row >= p.rows) return;   // whole waves; wider groups fill their block
   const int64_t cols = p.cols;
   float s[PER][8];
@@ -233,10 +233,10 @@ __global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_nor
 // Rows too long for registers: one block per row, three passes over it.
 constexpr int kLongThreads = 1024;
 template <bool F32>
-__global__ __launch_bounds__(kLongThreads) void layer_norm_long_kernel(NormFwd p) {
+__global__ __launch_bounds__(kLongThreads) void layer_norm_long_kernel(NormFwd p, int64_t row0) {
   constexpr int ES = F32 ? 4 : 2;
   __shared__ float s_red[2][kLongThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = row0 + blockIdx.x;
   const int wave = threadIdx.x >> 6;
   const char* xr = static_cast<const char*>(p.x) + row * p.ldx * ES;
   const char* rr = p.residual ? static_cast<const char*>(p.residual) + row * p.ldr * ES : nullptr;
@@ -274,16 +274,28 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // whether rows of `cols` elements of size es at p, ld apart, take 16-byte accesses
 bool row16(const void* p, int64_t ld, int es) { return !p || (al16(p) && ld * es % 16 == 0); }
 
+// A launch holds fewer than 2^32 threads: f(first row, rows of the launch) for
+// ranges of `rows` that take 2^31 at `threads` per row.
+template <typename F>
+hipError_t by_row_ranges(int64_t rows, int threads, F f) {
+  const int64_t step = (int64_t{1} << 31) / threads;
+  for (int64_t r = 0; r < rows; r += step) {
+    f(r, rows - r < step ? rows - r : step);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <bool F32, bool VEC>
 hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
   const bool gv = p.gamma && al16(p.gamma), bv = p.beta && al16(p.beta);
-#define DSMOE_LN(NT, PER)                                                                                    \
-  do {                                                                                                       \
-    constexpr int bt_ = NT > kFwdThreads ? NT : kFwdThreads;                                                 \
-    const int64_t grid_ = (p.rows + bt_ / NT - 1) / (bt_ / NT);                                              \
-    layer_norm_kernel<F32, VEC, NT, PER><<<static_cast<uint32_t>(grid_), bt_, 0, s>>>(p, gv, bv);            \
-    return hipGetLastError();                                                                                \
-  } while (0)
+#define DSMOE_LN(NT, PER)                                                                                \
+  return by_row_ranges(p.rows, NT, [&](int64_t r0, int64_t n) {                                          \
+    constexpr int bt = NT > kFwdThreads ? NT : kFwdThreads;                                              \
+    const uint32_t grid = static_cast<uint32_t>((n + bt / NT - 1) / (bt / NT));                          \
+    layer_norm_kernel<F32, VEC, NT, PER><<<grid, bt, 0, s>>>(p, r0, gv, bv);                             \
+  })
   if (p.cols <= 512) DSMOE_LN(64, 1);
   if (p.cols <= 1024) DSMOE_LN(64, 2);
   if (p.cols <= 2048) DSMOE_LN(256, 1);
@@ -292,8 +304,9 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
   if (p.cols <= 16384) DSMOE_LN(512, 4);
   if (p.cols <= 32768) DSMOE_LN(1024, 4);
 #undef DSMOE_LN
-  layer_norm_long_kernel<F32><<<static_cast<uint32_t>(p.rows), kLongThreads, 0, s>>>(p);
-  return hipGetLastError();
+  return by_row_ranges(p.rows, kLongThreads, [&](int64_t r0, int64_t n) {
+    layer_norm_long_kernel<F32><<<static_cast<uint32_t>(n), kLongThreads, 0, s>>>(p, r0);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -428,10 +441,10 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
 
 // Rows too long for registers: dx by one block per row, two passes over it...
 template <bool F32>
-__global__ __launch_bounds__(kLongThreads) void layer_norm_bwd_long_kernel(NormBwd p) {
+__global__ __launch_bounds__(kLongThreads) void layer_norm_bwd_long_kernel(NormBwd p, int64_t row0) {
   constexpr int ES = F32 ? 4 : 2;
   __shared__ float s_red[2 * (kLongThreads / 64)];
-  const int64_t row = blockIdx.x;
+  const int64_t row = row0 + blockIdx.x;
   const char* xr = static_cast<const char*>(p.x) + row * p.ldx * ES;
   const char* yr = static_cast<const char*>(p.dy) + row * p.lddy * ES;
   const char* sr = p.dsum ? static_cast<const char*>(p.dsum) + row * p.ldds * ES : nullptr;
@@ -553,7 +566,9 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t s) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
       }
-      layer_norm_bwd_long_kernel<F32><<<static_cast<uint32_t>(p.rows), kLongThreads, 0, s>>>(p);
+      return by_row_ranges(p.rows, kLongThreads, [&](int64_t r0, int64_t n) {
+        layer_norm_bwd_long_kernel<F32><<<static_cast<uint32_t>(n), kLongThreads, 0, s>>>(p, r0);
+      });
   }
   return hipGetLastError();
 }

@@ -298,6 +298,51 @@ def test_linear_offsets_past_32_bits(d):
     _grad_check(dx, dw, None, od.linear_backward(dy64, x64, w64), dy64, x64, w64, False, "f32", "f32", "past 32 bits")
 
 
+def _repeats(v, n):
+    """n rows that repeat v's, on the device."""
+    out = torch.empty((n,) + tuple(v.shape[1:]), dtype=v.dtype, device="cuda")
+    whole = n // v.shape[0]
+    out[:whole * v.shape[0]].view(whole, *v.shape).copy_(v.expand(whole, *v.shape))
+    out[whole * v.shape[0]:].copy_(v[:n - whole * v.shape[0]])
+    return out
+
+
+def _check_repeats(got, part, what):
+    """Rows of got against the checked result of the rows that they repeat:
+    both within a rounding of the same sums."""
+    n = part.shape[0]
+    lim = 2.05 * V * part.float().abs() + 2.0 ** -16
+    for r in range(0, got.shape[0], n):
+        g = got[r:r + n].float()
+        off = (g - part[:g.shape[0]].float()).abs() > lim[:g.shape[0]]
+        assert not bool(off.any()), f"{what}: rows from {r}"
+        del g, off
+
+
+def test_more_rows_than_threads_of_a_launch(d):
+    """Row counts whose threads would pass 2^32 in one launch."""
+    banner("rows past one launch")
+    r = np.random.default_rng(11)
+    n = (1 << 20) + 3
+    x, x64 = _mat(r, n, 8)
+    g, g64 = _vec(r, 8, 0.2, 1.0)
+    y, mean, rstd, _ = d.layer_norm(x, g)
+    _norm_fwd_check((y, mean, rstd, None), x64, None, g64, None, 1e-5, "bf16", "part")
+    rows = (1 << 26) + 7
+    many = d.layer_norm(_repeats(x, rows), g)
+    _check_repeats(many[0], y, "layer norm")
+    _check_repeats(many[1][:, None], mean[:, None], "mean")
+    del many
+    w, w64 = _mat(r, 8, 8)
+    y, _ = d.linear(x, w)
+    _linear_check(y, None, x64, w64, None, "none", None, "bf16", "part")
+    xs = _repeats(x, (1 << 30) + 77)
+    out = torch.empty_like(xs)
+    banner("linear of 2^30 + 77 rows")
+    d.linear(xs, w, y=out)
+    _check_repeats(out, y, "linear")
+
+
 def _grad_check(dx, dw, db, want, dy64, x64, w64, rounded, dxt, dwt, what):
     """want: (dx, dw, dbias, dz); rounded: dz reaches the products as bf16."""
     wx, ww, wb, dz = want
