@@ -639,6 +639,70 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs arg
   w.finish(acc);
 }
 
+// 128 x 256: S stages of LDS, whole chunks.  The two waves of a SIMD run half a
+// chunk apart, one multiplying while the other reads all of its part of the
+// chunk; the stage that both have read takes the chunk S - 1 ahead.  Reads and
+// products of a chunk are about as long (16 reads, 32 products a wave), so
+// this beats reads between a wave's own products: 4096 x 2048 x 7168 in 92 us
+// instead of 103, by W's columns 97 instead of 122.  With 128 x 128, half the
+// products per barrier, it loses (2048^3 24.2 us instead of 22.9).
+template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
+__global__ __launch_bounds__(64 * WM * WN) void dense_paired_kernel(TileArgs args) {
+  using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
+  constexpr int TM = T::TM, TN = T::TN, L = 2 * T::LA + 2 * T::LB;
+  static_assert(T::NW == 8, "two waves per SIMD");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(S)];
+  T w(args, s_mem);
+  typename T::Acc acc;
+  T::clear(acc);
+  bf16x8 fa[2][TM][2], fb[2][TN][2];
+
+#define DSMOE_COPY(stage) w.copy_a0(stage), w.copy_b0(stage), w.copy_b1(stage), w.copy_a1(stage)
+  for (int i = 0; i < S - 1; ++i) DSMOE_COPY(w.lds + i * T::kStage);
+  wait_copies<(S - 2) * L>();
+  block_barrier();
+  if (w.wave >= 4) block_barrier();
+  uint32_t st = w.lds, free = w.lds + (S - 1) * T::kStage;
+  for (int32_t c = w.c0; c < w.c1; ++c) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[h][i][kk] = w.ra.read(st, h ? T::kA1 : T::kA0, i, kk);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[h][j][kk] = w.rb.read(st, h ? T::kB1 : T::kB0, j, kk);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    // The last barrier was the other wave's end of reading the chunk before.
+    DSMOE_COPY(free);
+    wait_copies<(S - 2) * L>();   // this wave's part of the next chunk is there
+    wait_lds();
+    block_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+            acc[h >> 1][h & 1][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h & 1][j][kk], fa[h >> 1][i][kk],
+                                                                               acc[h >> 1][h & 1][i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    block_barrier();
+    free = st;
+    st = st + T::kStage == w.lds + S * T::kStage ? w.lds : st + T::kStage;
+  }
+#undef DSMOE_COPY
+  if (w.wave < 4) block_barrier();
+  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
+  w.finish(acc);
+}
+
 // Smaller tiles: S stages of LDS.  A chunk's fragments are read in two steps of
 // 32 of K, each while the products of the step before run; once a chunk's
 // second step is in registers in every wave, its stage is refilled with the
@@ -803,7 +867,7 @@ __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd
 //   256 x 192  phased: what is left over when 256 x 256 tiles fill the card a
 //              whole number of times (see make_plan), and sizes it fits better
 //   128 x 256  three stages, one per CU: when 256 x 256 leaves CUs without a
-//              tile (4096 x 2048 x 7168 in 103 us; 128 x 128 117, 256 x 256 173)
+//              tile (4096 x 2048 x 7168 in 92 us; 128 x 128 117, 256 x 256 173)
 //   64 x 64    four stages, two per CU: small products
 //              (1024^3 in 9.5 us; 128 x 128 12.8)
 enum class Shape { k256, k256x192, k128x256, k128x4, k128x2, k64 };
@@ -813,7 +877,7 @@ struct ShapeInfo {
   double chunk_us, shared_us, end_us;
 };
 constexpr ShapeInfo kShapes[] = {
-    {256, 256, 1, 1.42, 0.0, 5.0}, {256, 192, 1, 1.12, 0.0, 4.5},  {128, 256, 1, 0.88, 0.0, 4.0},
+    {256, 256, 1, 1.42, 0.0, 5.0}, {256, 192, 1, 1.12, 0.0, 4.5},  {128, 256, 1, 0.79, 0.0, 4.0},
     {128, 128, 1, 0.50, 0.0, 3.0}, {128, 128, 2, 0.60, 1.00, 3.0}, {64, 64, 2, 0.30, 0.42, 2.0}};
 constexpr int64_t kCus = 256;
 constexpr double kHbm = 4.8e6;   // bytes per us of a long read
@@ -919,6 +983,8 @@ hipError_t launch_kernel(const TileArgs& t, hipStream_t s) {
   constexpr int threads = 64 * WM * WN;
   if constexpr (HM == 128)
     dense_phased_kernel<HM, HN, WM, WN, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
+  else if constexpr (HN == 128)
+    dense_paired_kernel<HM, HN, WM, WN, S, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   else
     dense_ring_kernel<HM, HN, WM, WN, S, AT, BT, EPI><<<grid, threads, 0, s>>>(t);
   return hipGetLastError();
