@@ -27,12 +27,11 @@
 #include "common.h"
 #include "dense.h"
 #include "dense_epi.h"
+#include "vec8.h"
 
 namespace dsmoe {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -51,42 +50,11 @@ constexpr int kXcds = 8;
 // Epilogue: 8 adjacent columns of one row.
 // ---------------------------------------------------------------------------
 
-// columns i .. i + 7 of a matrix at base (f32 or bf16), 16-byte accesses
-__device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, float* o) {
-  if (f32) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
-    const f32x4 a = q[0], b = q[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[2 * e] = __uint_as_float(a[e] << 16);
-      o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ void store8(void* base, int64_t i, bool f32, const float* v) {
-  if (f32) {
-    f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + i);
-    q[0] = f32x4{v[0], v[1], v[2], v[3]};
-    q[1] = f32x4{v[4], v[5], v[6], v[7]};
-  } else {
-    u32x4 a;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + i) = a;
-  }
-}
-
 struct TileArgs {
   DenseGemm p;
   int64_t a_k, b_k;       // contraction length readable along a row (row operands: a multiple of 8)
   int64_t a_r, b_r;       // rows readable (k-row operands: a multiple of 8; kGated: of one half of b)
-  bool vec;               // every matrix of the epilogue takes 16-byte accesses, in whole runs of 8 columns
-  bool plain;             // kLinear: one split, no activation or z, whole vectors
+  bool plain;             // kLinear: one split, no activation or z
   float* partial;         // splits > 1: [split][M][ldp] partial sums, no epilogue
   int64_t ldp;            // (kGated: gate sums, then up sums at + N rounded up to 8)
   int32_t splits;
@@ -94,13 +62,14 @@ struct TileArgs {
   int32_t tiles_m, tiles_n;
 };
 
-// Whole runs of 8 columns: y = act(acc + bias) + residual, z = acc + bias
+// y = act(acc + bias) + residual, z = acc + bias
 __device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int64_t n, float* v, const float* bias) {
+  const int64_t left = p.N - n;
   float r[8];
-  if (p.residual) load8(p.residual, m * p.ldr + n, p.y_f32, r);
+  if (p.residual) load8(p.residual, m * p.ldr + n, p.y_f32, left, r);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] += bias[e];
-  if (p.z) store8(p.z, m * p.ldz + n, p.y_f32, v);
+  if (p.z) store8(p.z, m * p.ldz + n, p.y_f32, left, v);
   if (p.act != DSMOE_ACT_NONE) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, v[e]);
@@ -109,28 +78,28 @@ __device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  store8(p.y, m * p.ldy + n, p.y_f32, v);
+  store8(p.y, m * p.ldy + n, p.y_f32, left, v);
 }
 
 // a = act(g) u, h = [g | u]
 __device__ __forceinline__ void finish_gated(const DenseGemm& p, int64_t m, int64_t n, const float* g, const float* u) {
+  const int64_t left = p.N - n;
   if (p.z) {
-    store8(p.z, m * p.ldz + n, false, g);
-    store8(p.z, m * p.ldz + p.gate_n + n, false, u);
+    store8(p.z, m * p.ldz + n, false, left, g);
+    store8(p.z, m * p.ldz + p.gate_n + n, false, left, u);
   }
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, g[e]) * u[e];
-  store8(p.y, m * p.ldy + n, p.y_f32, v);
+  store8(p.y, m * p.ldy + n, p.y_f32, left, v);
 }
 
 __device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* o) {
+  if (p.bias) {
+    load8(p.bias, n, p.bias_f32, p.N - n, o);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    o[e] = 0.0f;
-    if (p.bias && n + e < p.N)
-      o[e] = p.bias_f32 ? static_cast<const float*>(p.bias)[n + e]
-                        : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n + e]);
+    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
   }
 }
 
@@ -429,30 +398,25 @@ struct Tile {
     for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
   }
 
-  // y = acc + bias + residual with whole aligned runs.  The residual of all of
+  // y = acc + bias + residual.  The residual of all of
   // a thread's rows is on its way before the results are in LDS (bf16: of both
   // halves; a batch of four rows at a time between the stores cost 4096 x 7168
   // x 2048 with a residual 27 us over the same without).
   template <bool F32>
   __device__ __forceinline__ void finish_plain(const Acc& acc) const {
-    constexpr int R = HM / kRowsAtOnce, Q = F32 ? 2 : 1, ES = F32 ? 4 : 2;
+    constexpr int R = HM / kRowsAtOnce, ES = F32 ? 4 : 2;
     const int run = threadIdx.x % kRuns, r0 = threadIdx.x / kRuns;
     const int64_t n = n0 + run * 8;
     const bool in = n < p.N && r0 < kRowsAtOnce;
     float bias[8];
     load_bias(p, n, bias);
-    u32x4 res[2][R][Q];
+    Raw8<F32> res[2][R];
     auto fetch = [&](int ha) {
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         const int64_t m = m0 + ha * HM + r0 + q * kRowsAtOnce;
-#pragma unroll
-        for (int h = 0; h < Q; ++h) res[ha][q][h] = u32x4{0, 0, 0, 0};
-        if (p.residual && in && m < p.M) {
-          const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const char*>(p.residual) + (m * p.ldr + n) * ES);
-#pragma unroll
-          for (int h = 0; h < Q; ++h) res[ha][q][h] = from[h];
-        }
+        const bool some = p.residual && in && m < p.M;
+        res[ha][q] = fetch8<F32>(static_cast<const char*>(p.residual) + (m * p.ldr + n) * ES, some ? p.N - n : 0);
       }
     };
     fetch(0);
@@ -467,18 +431,12 @@ struct Tile {
         const int r = r0 + q * kRowsAtOnce;
         const int64_t m = m0 + ha * HM + r;
         if (m >= p.M) break;
-        float v[8];
+        float v[8], x[8];
         get(r, run * 8, v);
+        unpack8<F32>(res[ha][q], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x;
-          if constexpr (F32)
-            x = __uint_as_float(res[ha][q][e / 4][e % 4]);
-          else
-            x = __uint_as_float(e % 2 ? res[ha][q][0][e / 2] & 0xffff0000u : res[ha][q][0][e / 2] << 16);
-          v[e] = v[e] + bias[e] + x;
-        }
-        store8(p.y, m * p.ldy + n, F32, v);
+        for (int e = 0; e < 8; ++e) v[e] = v[e] + bias[e] + x[e];
+        store8(p.y, m * p.ldy + n, F32, p.N - n, v);
       }
     }
   }
@@ -494,58 +452,28 @@ struct Tile {
       }
     }
     const int64_t half_n = (p.N + 7) / 8 * 8;   // columns of partial sums of a kind, padded
-    const bool runs = t.splits > 1 || t.vec;
     const int run = threadIdx.x % kRuns;
     const int64_t n = n0 + run * 8;
     float bias[8] = {};
-    if (!kGated && t.splits == 1 && t.vec) load_bias(p, n, bias);
+    if (!kGated && t.splits == 1) load_bias(p, n, bias);
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
       put(acc[ha]);
-      if (runs) {
-        if (static_cast<int>(threadIdx.x) >= kRowsAtOnce * kRuns) continue;
+      if (static_cast<int>(threadIdx.x) >= kRowsAtOnce * kRuns) continue;
 #pragma unroll 1
-        for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
-          const int64_t m = m0 + ha * HM + r;
-          if (m >= p.M || n >= half_n) break;
-          float v[8], u[8];
-          get(r, run * 8, v);
-          if constexpr (kGated) get(r, HN + run * 8, u);
-          if (t.splits > 1) {
-            store8(t.partial, (split * p.M + m) * t.ldp + n, true, v);
-            if constexpr (kGated) store8(t.partial, (split * p.M + m) * t.ldp + half_n + n, true, u);
-          } else if constexpr (kGated) {
-            finish_gated(p, m, n, v, u);
-          } else {
-            finish_linear(p, m, n, v, bias);
-          }
-        }
-      } else {
-        // rows of no alignment: one column per thread, adjacent lanes adjacent
-        // columns, the residuals of kBatch rows loaded first
-        constexpr int kCols = kRuns * 8, kRows = rows_at_once(kCols), kBatch = HM / kRows < 4 ? HM / kRows : 4;
-        static_assert(HM % (kRows * kBatch) == 0, "whole batches");
-        const int c = threadIdx.x % kCols;
-        if (n0 + c >= p.N || static_cast<int>(threadIdx.x) >= kRows * kCols) continue;
-#pragma unroll 1
-        for (int r0 = threadIdx.x / kCols; r0 < HM; r0 += kRows * kBatch) {
-          const int64_t m1 = m0 + ha * HM + r0;
-          float res[kBatch];
-          if (!kGated && p.residual) {
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-              res[q] = m1 + q * kRows < p.M ? load1(p.residual, (m1 + q * kRows) * p.ldr + n0 + c, p.y_f32) : 0.0f;
-          }
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const int64_t m = m1 + q * kRows;
-            if (m >= p.M) break;
-            const uint32_t at = lds + ((r0 + q * kRows) * kOutStride + c) * 4;
-            if constexpr (kGated)
-              finish_gated1(p, m, n0 + c, *lds_ptr<const float>(at), *lds_ptr<const float>(at + HN * 4));
-            else
-              finish_linear1(p, m, n0 + c, *lds_ptr<const float>(at), res[q]);
-          }
+      for (int r = threadIdx.x / kRuns; r < HM; r += kRowsAtOnce) {
+        const int64_t m = m0 + ha * HM + r;
+        if (m >= p.M || n >= half_n) break;
+        float v[8], u[8];
+        get(r, run * 8, v);
+        if constexpr (kGated) get(r, HN + run * 8, u);
+        if (t.splits > 1) {
+          put8<true>(t.partial + (split * p.M + m) * t.ldp + n, 8, v);
+          if constexpr (kGated) put8<true>(t.partial + (split * p.M + m) * t.ldp + half_n + n, 8, u);
+        } else if constexpr (kGated) {
+          finish_gated(p, m, n, v, u);
+        } else {
+          finish_linear(p, m, n, v, bias);
         }
       }
     }
@@ -778,7 +706,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(TileArgs t) {
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int k = 0; k < kKinds; ++k)
-        if (s + q < t.splits) load8(t.partial + ((s + q) * p.M + m) * t.ldp + k * runs * 8, n, true, o[q][k]);
+        if (s + q < t.splits) load8(t.partial + ((s + q) * p.M + m) * t.ldp + k * runs * 8, n, true, 8, o[q][k]);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (s + q < t.splits) {
@@ -788,28 +716,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(TileArgs t) {
           for (int e = 0; e < 8; ++e) v[k][e] += o[q][k][e];
       }
   }
-  if (t.vec) {
-    if constexpr (EPI == DenseEpi::kGated) {
-      finish_gated(p, m, n, v[0], v[1]);
-    } else {
-      float bias[8];
-      load_bias(p, n, bias);
-      finish_linear(p, m, n, v[0], bias);
-    }
+  if constexpr (EPI == DenseEpi::kGated) {
+    finish_gated(p, m, n, v[0], v[1]);
   } else {
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      if (n + e >= p.N) break;
-      // v is indexed by constants only
-      float g = 0.0f, u = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q == e) g = v[0][q], u = v[kKinds - 1][q];
-      if constexpr (EPI == DenseEpi::kGated)
-        finish_gated1(p, m, n + e, g, u);
-      else
-        finish_linear1(p, m, n + e, g, p.residual ? load1(p.residual, m * p.ldr + n + e, p.y_f32) : 0.0f);
-    }
+    float bias[8];
+    load_bias(p, n, bias);
+    finish_linear(p, m, n, v[0], bias);
   }
 }
 
@@ -830,12 +742,7 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(PackArgs a) {
        i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t r = i >> 32 ? i / segs : static_cast<uint32_t>(i) / static_cast<uint32_t>(segs);
     const int64_t c = (i - r * segs) * 8;
-    const uint16_t* q = src + r * lds + c;
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? q[e] : 0;
-    *reinterpret_cast<u32x4*>(dst + r * segs * 8 + c) =
-        u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+    *reinterpret_cast<u32x4*>(dst + r * segs * 8 + c) = fetch8<false>(src + r * lds + c, cols - c).q[0];
   }
 }
 
@@ -1043,12 +950,10 @@ hipError_t launch_range(const DenseGemm& p, hipStream_t s) {
   t.b_k = p.b.k_rows ? p.K : up8(p.K);
   t.a_r = p.a.k_rows ? up8(p.M) : p.M;
   t.b_r = p.b.k_rows ? up8(p.N) : p.N;
-  t.vec = row16(p.y, p.ldy, p.y_f32 ? 4 : 2) && row16(p.residual, p.ldr, p.y_f32 ? 4 : 2) &&
-          row16(p.z, p.ldz, !gated && p.y_f32 ? 4 : 2) && p.N % 8 == 0;
   t.chunks = static_cast<int32_t>(pl.chunks);
   auto run = [&](const Grid& g) {
     t.splits = g.splits;
-    t.plain = g.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z && t.vec;
+    t.plain = g.splits == 1 && p.act == DSMOE_ACT_NONE && !p.z;
     t.tiles_m = static_cast<int32_t>(g.tiles_m);
     t.tiles_n = static_cast<int32_t>(g.tiles_n);
     switch (g.shape) {

@@ -8,57 +8,18 @@
 #include "act.h"
 #include "common.h"
 #include "dense.h"
+#include "vec8.h"
 
 namespace dsmoe {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// 8 columns of a row from column c (c < n): one 16-byte access per 16 bytes
-// when vec (n a multiple of 8 and the row 16-byte aligned), else one by one,
-// 0 past the row's end
-template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int64_t c, int64_t n, bool vec, float* o) {
-  if (vec) {
-    if constexpr (F32) {
-      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
-      const f32x4 a = q[0], b = q[1];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = a[e], o[4 + e] = b[e];
-    } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[2 * e] = __uint_as_float(a[e] << 16);
-        o[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (F32)
-        o[e] = c + e < n ? static_cast<const float*>(row)[c + e] : 0.0f;
-      else
-        o[e] = c + e < n ? bf16_to_f32(static_cast<const uint16_t*>(row)[c + e]) : 0.0f;
-    }
-  }
-}
-
-__device__ __forceinline__ u32x4 pack8(const float* v) {
-  u32x4 a;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-  return a;
-}
 
 // A block takes `ct` slots of 8 columns (a power of 2, 32 at most) and the rows
 // of strip blockIdx.y, 256 / ct of them at a time, two such steps of loads in
 // flight; its threads' column sums are joined through LDS.
 template <bool ZF32>
 __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
-                                                           const void* __restrict__ z, int64_t ldz, bool vec,
-                                                           int act, int64_t M, int64_t N, int ct, int64_t strip,
+                                                           const void* __restrict__ z, int64_t ldz, int act,
+                                                           int64_t M, int64_t N, int ct, int64_t strip,
                                                            uint16_t* __restrict__ dz, int64_t lddz,
                                                            float* __restrict__ partial) {
   __shared__ float s_sum[256 * 8];
@@ -70,10 +31,10 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
 #pragma unroll 2
     for (int64_t r = blockIdx.y * strip + threadIdx.x / ct; r < r1; r += rt) {
       float g[8];
-      load8<false>(dy + r * lddy, c, N, vec, g);
+      unpack8<false>(fetch8<false>(dy + r * lddy + c, N - c), g);
       if (z) {
         float zz[8];
-        load8<ZF32>(static_cast<const char*>(z) + r * ldz * (ZF32 ? 4 : 2), c, N, vec, zz);
+        unpack8<ZF32>(fetch8<ZF32>(static_cast<const char*>(z) + (r * ldz + c) * (ZF32 ? 4 : 2), N - c), zz);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float f, d;
@@ -109,8 +70,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
 
 // One slot of 8 columns of da per thread and pass over the grid.
 __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __restrict__ da, int64_t ldda,
-                                                             const uint16_t* __restrict__ h, int64_t ldh, bool vec,
-                                                             int act, int64_t M, int64_t I,
+                                                             const uint16_t* __restrict__ h, int64_t ldh, int act,
+                                                             int64_t M, int64_t I,
                                                              uint16_t* __restrict__ dh, int64_t lddh) {
   const uint32_t slots = static_cast<uint32_t>((I + 7) / 8);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < M * slots;
@@ -119,9 +80,9 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __r
     const int64_t r = i >> 32 ? i / slots : static_cast<uint32_t>(i) / slots;
     const int64_t c = 8 * (i - r * slots);
     float d[8], g[8], u[8], dg[8], du[8];
-    load8<false>(da + r * ldda, c, I, vec, d);
-    load8<false>(h + r * ldh, c, I, vec, g);
-    load8<false>(h + r * ldh + I, c, I, vec, u);
+    unpack8<false>(fetch8<false>(da + r * ldda + c, I - c), d);
+    unpack8<false>(fetch8<false>(h + r * ldh + c, I - c), g);
+    unpack8<false>(fetch8<false>(h + r * ldh + I + c, I - c), u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float f, df;
@@ -130,28 +91,15 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __r
       du[e] = d[e] * f;
     }
     uint16_t* o = dh + r * lddh + c;
-    if (vec) {
-      *reinterpret_cast<u32x4*>(o) = pack8(dg);
-      *reinterpret_cast<u32x4*>(o + I) = pack8(du);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < I) {
-          o[e] = static_cast<uint16_t>(f32x2_to_bf16x2(dg[e], 0.0f));
-          o[I + e] = static_cast<uint16_t>(f32x2_to_bf16x2(du[e], 0.0f));
-        }
-      // the row's padding past 2 I, by the thread that owns the last column
-      if (c + 8 >= I)
-        for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
-    }
+    put8<false>(o, I - c, dg);
+    put8<false>(o + I, I - c, du);
+    // the row's padding past 2 I, by the thread that owns the last column
+    if (c + 8 >= I)
+      for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
   }
 }
 
 constexpr int64_t kMaxBlocks = 1 << 23;   // 2^31 threads; a launch holds fewer than 2^32
-
-bool row16(const void* p, int64_t ld, int es) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
-}
 
 // column slots of a block of act_backward_kernel, rows of a strip: about 1024
 // blocks, of at least two steps of rows each
@@ -178,24 +126,22 @@ int64_t bias_partial_rows(int64_t M, int64_t N) {
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz, bool z_f32, int act,
                                int64_t M, int64_t N, uint16_t* dz, int64_t lddz, float* partial, hipStream_t s) {
   if (M == 0) return hipSuccess;
-  const bool vec = N % 8 == 0 && row16(dy, lddy, 2) && row16(z, ldz, z_f32 ? 4 : 2);
   const int ct = column_slots(N);
   const int64_t strip = strip_rows(M, N);
   const dim3 grid(static_cast<uint32_t>((N + 8 * ct - 1) / (8 * ct)), static_cast<uint32_t>((M + strip - 1) / strip));
   if (z_f32)
-    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, ct, strip, dz, lddz, partial);
+    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, lddz, partial);
   else
-    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, vec, act, M, N, ct, strip, dz, lddz, partial);
+    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, lddz, partial);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_t* h, int64_t ldh, int act,
                                  int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s) {
   if (M == 0) return hipSuccess;
-  const bool vec = I % 8 == 0 && row16(da, ldda, 2) && row16(h, ldh, 2);
   const int64_t all = (M * ((I + 7) / 8) + 255) / 256;
   const uint32_t blocks = static_cast<uint32_t>(all < kMaxBlocks ? all : kMaxBlocks);
-  gated_backward_kernel<<<blocks, 256, 0, s>>>(da, ldda, h, ldh, vec, act, M, I, dh, lddh);
+  gated_backward_kernel<<<blocks, 256, 0, s>>>(da, ldda, h, ldh, act, M, I, dh, lddh);
   return hipGetLastError();
 }
 

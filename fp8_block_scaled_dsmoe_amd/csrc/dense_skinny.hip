@@ -16,39 +16,17 @@
 #include "common.h"
 #include "dense.h"
 #include "dense_epi.h"
+#include "vec8.h"
 
 namespace dsmoe {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 values from q; VEC: one 16-byte load
-template <bool VEC>
-__device__ __forceinline__ u32x4 load_frag(const uint16_t* q) {
-  if constexpr (VEC) {
-    return *reinterpret_cast<const u32x4*>(q);
-  } else {
-    u32x4 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = q[2 * e] | static_cast<uint32_t>(q[2 * e + 1]) << 16;
-    return r;
-  }
-}
-// the first `left` (0 to 7) of 8 values, the others 0
-__device__ __forceinline__ u32x4 load_tail(const uint16_t* q, int left) {
-  u32x4 r;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t lo = 2 * e < left ? q[2 * e] : 0, hi = 2 * e + 1 < left ? q[2 * e + 1] : 0;
-    r[e] = lo | hi << 16;
-  }
-  return r;
-}
+__device__ __forceinline__ u32x4 load_frag(const uint16_t* q) { return *reinterpret_cast<const u32x4_at2*>(q); }
 
 // MT: groups of 16 tokens; DEPTH: steps of K in flight per wave.
-template <int MT, int DEPTH, int kWaves, bool VEC, DenseEpi EPI>
+template <int MT, int DEPTH, int kWaves, DenseEpi EPI>
 __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) {
   constexpr bool kGated = EPI == DenseEpi::kGated;
   constexpr int kCols = kGated ? 8 : 16;   // result columns of the block
@@ -89,11 +67,11 @@ __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) 
   auto fetch = [&](int d, int s) {
     const int64_t at = static_cast<int64_t>(s) * 64;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) fw[d][h] = load_frag<VEC>(wp + at + 8 * h);
+    for (int h = 0; h < 2; ++h) fw[d][h] = load_frag(wp + at + 8 * h);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fx[d][t][h] = load_frag<VEC>(xp[t] + at + 8 * h);
+      for (int h = 0; h < 2; ++h) fx[d][t][h] = load_frag(xp[t] + at + 8 * h);
   };
   auto multiply = [&](int d) {
 #pragma unroll
@@ -119,13 +97,8 @@ __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) 
     const int64_t at = static_cast<int64_t>(n_steps) * 64;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t rest = p.K - k0 - at - 8 * h;   // valid k from this lane's 8 on
-      const int left = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), rest)));
-      auto load = [&](const uint16_t* q) {
-        if (left == 8) return load_frag<VEC>(q + at + 8 * h);
-        if (left > 0) return load_tail(q + at + 8 * h, left);
-        return u32x4{0, 0, 0, 0};
-      };
+      const int64_t left = p.K - k0 - at - 8 * h;   // valid k from this lane's 8 on
+      auto load = [&](const uint16_t* q) { return fetch8<false>(q + at + 8 * h, left).q[0]; };
       const u32x4 a = load(wp);
 #pragma unroll
       for (int t = 0; t < MT; ++t) product(a, load(xp[t]), acc[t]);
@@ -155,33 +128,26 @@ __global__ __launch_bounds__(64 * kWaves) void dense_skinny_kernel(DenseGemm p) 
   }
 }
 
-template <int MT, int DEPTH, int kWaves, bool VEC>
+template <int MT, int DEPTH, int kWaves>
 hipError_t launch_mt(const DenseGemm& p, hipStream_t s) {
   const int cols = p.epi == DenseEpi::kGated ? 8 : 16;
   const uint32_t grid = static_cast<uint32_t>((p.N + cols - 1) / cols);
   if (p.epi == DenseEpi::kGated)
-    dense_skinny_kernel<MT, DEPTH, kWaves, VEC, DenseEpi::kGated><<<grid, 64 * kWaves, 0, s>>>(p);
+    dense_skinny_kernel<MT, DEPTH, kWaves, DenseEpi::kGated><<<grid, 64 * kWaves, 0, s>>>(p);
   else
-    dense_skinny_kernel<MT, DEPTH, kWaves, VEC, DenseEpi::kLinear><<<grid, 64 * kWaves, 0, s>>>(p);
+    dense_skinny_kernel<MT, DEPTH, kWaves, DenseEpi::kLinear><<<grid, 64 * kWaves, 0, s>>>(p);
   return hipGetLastError();
 }
-
-template <bool VEC>
-hipError_t launch_vec(const DenseGemm& p, hipStream_t s) {
-  // more token groups need more registers per step: fewer waves, same bytes in
-  // flight
-  if (p.M <= 16) return launch_mt<1, 4, 16, VEC>(p, s);
-  if (p.M <= 32) return launch_mt<2, 3, 16, VEC>(p, s);
-  if (p.M <= 48) return launch_mt<3, 4, 8, VEC>(p, s);
-  return launch_mt<4, 3, 8, VEC>(p, s);
-}
-
-bool row16(const Operand& o) { return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.ld % 8 == 0; }
 
 }  // namespace
 
 hipError_t launch_dense_skinny(const DenseGemm& p, hipStream_t s) {
-  return row16(p.a) && row16(p.b) ? launch_vec<true>(p, s) : launch_vec<false>(p, s);
+  // more token groups need more registers per step: fewer waves, same bytes in
+  // flight
+  if (p.M <= 16) return launch_mt<1, 4, 16>(p, s);
+  if (p.M <= 32) return launch_mt<2, 3, 16>(p, s);
+  if (p.M <= 48) return launch_mt<3, 4, 8>(p, s);
+  return launch_mt<4, 3, 8>(p, s);
 }
 
 }  // namespace dsmoe

@@ -15,12 +15,10 @@
 
 #include "common.h"
 #include "dense.h"
+#include "vec8.h"
 
 namespace dsmoe {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return static_cast<uint16_t>(f32x2_to_bf16x2(v, 0.0f)); }
 
@@ -29,107 +27,37 @@ __device__ __forceinline__ float load1(const void* p, int64_t i, bool f32) {
 }
 
 // A row of up to NT * 8 * PER values over NT threads: slot v of thread t holds
-// 8 values.  VEC: columns 8 (v NT + t) + [0, 8), moved as 16-byte accesses
-// (two for float32); needs 16-byte aligned rows of a multiple of 8 columns.
-// Otherwise value e is column (8 v + e) NT + t, moved one by one.
-template <bool F32, bool VEC, int NT>
+// columns 8 (v NT + t) + [0, 8), those past cols 0.
+template <bool F32, int NT>
 struct Row {
-  static __device__ __forceinline__ int64_t col(int v, int e, int t) {
-    return VEC ? 8 * (static_cast<int64_t>(v) * NT + t) + e : (8 * static_cast<int64_t>(v) + e) * NT + t;
-  }
-  // 8 values as loaded: bf16 pairs, or float32
-  struct Raw {
-    u32x4 q[F32 ? 2 : 1];
-  };
-  // slot v of the row at base (those past cols read 0)
+  using Raw = Raw8<F32>;
+  static constexpr int ES = F32 ? 4 : 2;
+  static __device__ __forceinline__ int64_t col(int v, int t) { return 8 * (static_cast<int64_t>(v) * NT + t); }
   static __device__ __forceinline__ Raw fetch(const void* base, int v, int t, int64_t cols) {
-    Raw r;
-    if constexpr (VEC) {
-      const int64_t c = col(v, 0, t);
-      const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const char*>(base) + c * (F32 ? 4 : 2));
-#pragma unroll
-      for (int h = 0; h < (F32 ? 2 : 1); ++h) r.q[h] = c < cols ? q[h] : u32x4{0, 0, 0, 0};
-    } else if constexpr (F32) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col(v, e, t);
-        r.q[e / 4][e % 4] = c < cols ? static_cast<const uint32_t*>(base)[c] : 0;
-      }
-    } else {
-      uint32_t h[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col(v, e, t);
-        h[e] = c < cols ? static_cast<const uint16_t*>(base)[c] : 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r.q[0][e] = h[2 * e] | h[2 * e + 1] << 16;
-    }
-    return r;
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float* o) {
-    if constexpr (F32) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(r.q[e / 4][e % 4]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[2 * e] = __uint_as_float(r.q[0][e] << 16);
-        o[2 * e + 1] = __uint_as_float(r.q[0][e] & 0xffff0000u);
-      }
-    }
+    const int64_t c = col(v, t);
+    return fetch8<F32>(static_cast<const char*>(base) + c * ES, cols - c);
   }
   static __device__ __forceinline__ void load(const void* base, int v, int t, int64_t cols, float* o) {
-    unpack(fetch(base, v, t, cols), o);
+    unpack8<F32>(fetch(base, v, t, cols), o);
   }
   static __device__ __forceinline__ void store(void* base, int v, int t, int64_t cols, const float* o) {
-    if constexpr (VEC) {
-      const int64_t c = col(v, 0, t);
-      if (c >= cols) return;
-      if constexpr (F32) {
-        f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + c);
-        q[0] = f32x4{o[0], o[1], o[2], o[3]};
-        q[1] = f32x4{o[4], o[5], o[6], o[7]};
-      } else {
-        u32x4 a;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = f32x2_to_bf16x2(o[2 * e], o[2 * e + 1]);
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + c) = a;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col(v, e, t);
-        if (c >= cols) continue;
-        if constexpr (F32)
-          static_cast<float*>(base)[c] = o[e];
-        else
-          static_cast<uint16_t*>(base)[c] = f32_to_bf16(o[e]);
-      }
-    }
+    const int64_t c = col(v, t);
+    if (c < cols) put8<F32>(static_cast<char*>(base) + c * ES, cols - c, o);
   }
-  static __device__ __forceinline__ bool in(int v, int e, int t, int64_t cols) { return col(v, e, t) < cols; }
+  static __device__ __forceinline__ bool in(int v, int e, int t, int64_t cols) { return col(v, t) + e < cols; }
 };
 
-// slot v of a parameter vector: 16-byte loads where the rows take them and
-// the parameter's own pointer is aligned (pvec), else one by one
-template <bool F32, bool VEC, int NT>
-__device__ __forceinline__ void load_param(const void* p, bool p_f32, bool pvec, float missing, int v, int t,
-                                           int64_t cols, float* o) {
+// slot v of a parameter vector
+template <int NT>
+__device__ __forceinline__ void load_param(const void* p, bool p_f32, float missing, int v, int t, int64_t cols,
+                                           float* o) {
   if (!p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = missing;
-  } else if (VEC && pvec) {
-    if (p_f32)
-      Row<true, VEC, NT>::load(p, v, t, cols, o);
-    else
-      Row<false, VEC, NT>::load(p, v, t, cols, o);
+  } else if (p_f32) {
+    Row<true, NT>::load(p, v, t, cols, o);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c = Row<F32, VEC, NT>::col(v, e, t);
-      o[e] = c < cols ? load1(p, c, p_f32) : 0.0f;
-    }
+    Row<false, NT>::load(p, v, t, cols, o);
   }
 }
 
@@ -166,12 +94,11 @@ __device__ __forceinline__ void group_sum(float* v, float* scratch, int wave) {
 constexpr int kFwdThreads = 256;
 
 // One row per NT threads.
-template <bool F32, bool VEC, int NT, int PER>
-__global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_norm_kernel(NormFwd p, int64_t row0,
-                                                                                         bool gvec, bool bvec) {
+template <bool F32, int NT, int PER>
+__global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_norm_kernel(NormFwd p, int64_t row0) {
   constexpr int BT = NT > kFwdThreads ? NT : kFwdThreads;
   constexpr int ES = F32 ? 4 : 2;
-  using R = Row<F32, VEC, NT>;
+  using R = Row<F32, NT>;
   __shared__ float s_red[2][BT / 64];
   const int wave = threadIdx.x >> 6;
   const int t = threadIdx.x % NT;
@@ -218,8 +145,8 @@ __global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_nor
 #pragma unroll
   for (int v = 0; v < PER; ++v) {
     float ga[8], be[8], o[8];
-    load_param<F32, VEC, NT>(p.gamma, p.p_f32, gvec, 1.0f, v, t, cols, ga);
-    load_param<F32, VEC, NT>(p.beta, p.p_f32, bvec, 0.0f, v, t, cols, be);
+    load_param<NT>(p.gamma, p.p_f32, 1.0f, v, t, cols, ga);
+    load_param<NT>(p.beta, p.p_f32, 0.0f, v, t, cols, be);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(s[v][e] * rstd, ga[e], be[e]);
     R::store(yr, v, t, cols, o);
@@ -270,10 +197,6 @@ __global__ __launch_bounds__(kLongThreads) void layer_norm_long_kernel(NormFwd p
   }
 }
 
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-// whether rows of `cols` elements of size es at p, ld apart, take 16-byte accesses
-bool row16(const void* p, int64_t ld, int es) { return !p || (al16(p) && ld * es % 16 == 0); }
-
 // A launch holds fewer than 2^32 threads: f(first row, rows of the launch) for
 // ranges of `rows` that take 2^31 at `threads` per row.
 template <typename F>
@@ -287,14 +210,13 @@ hipError_t by_row_ranges(int64_t rows, int threads, F f) {
   return hipSuccess;
 }
 
-template <bool F32, bool VEC>
+template <bool F32>
 hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
-  const bool gv = p.gamma && al16(p.gamma), bv = p.beta && al16(p.beta);
 #define DSMOE_LN(NT, PER)                                                                                \
   return by_row_ranges(p.rows, NT, [&](int64_t r0, int64_t n) {                                          \
     constexpr int bt = NT > kFwdThreads ? NT : kFwdThreads;                                              \
     const uint32_t grid = static_cast<uint32_t>((n + bt / NT - 1) / (bt / NT));                          \
-    layer_norm_kernel<F32, VEC, NT, PER><<<grid, bt, 0, s>>>(p, r0, gv, bv);                             \
+    layer_norm_kernel<F32, NT, PER><<<grid, bt, 0, s>>>(p, r0);                                          \
   })
   if (p.cols <= 512) DSMOE_LN(64, 1);
   if (p.cols <= 1024) DSMOE_LN(64, 2);
@@ -321,11 +243,11 @@ constexpr int kBwdThreads = 512;
 constexpr int64_t kBwdBlocks = 256;
 
 // PER: slots of 8 columns per thread
-template <bool F32, bool VEC, int NT, int PER>
-__global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, bool gvec) {
+template <bool F32, int NT, int PER>
+__global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p) {
   constexpr int BT = kBwdThreads, RG = BT / NT;
   constexpr int ES = F32 ? 4 : 2;
-  using R = Row<F32, VEC, NT>;
+  using R = Row<F32, NT>;
   __shared__ float s_red[2][2 * (BT / 64)];
   __shared__ float s_part[RG > 1 ? BT * PER * 8 : 1];
   const int wave = threadIdx.x >> 6;
@@ -335,13 +257,14 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
   float ga[PER][8], dga[PER][8], dbe[PER][8];
 #pragma unroll
   for (int v = 0; v < PER; ++v) {
-    load_param<F32, VEC, NT>(p.gamma, p.p_f32, gvec, 1.0f, v, t, cols, ga[v]);
+    load_param<NT>(p.gamma, p.p_f32, 1.0f, v, t, cols, ga[v]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dga[v][e] = dbe[v][e] = 0.0f;
   }
   // The next row is fetched before this one is finished: with the loads of a
   // row waited for in turn, two blocks per CU kept too few bytes on the way
   // (4096 x 7168 bf16 with dsum took 103 us).
+  constexpr bool kAhead = PER <= 2;   // beyond, there are no registers left for it
   typename R::Raw nx[PER], ny[PER], nd[PER];
   float nmean = 0.0f, nrstd = 0.0f;
   auto fetch = [&](int64_t row) {
@@ -352,10 +275,9 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
     for (int v = 0; v < PER; ++v) {
       nx[v] = R::fetch(static_cast<const char*>(p.x) + row * p.ldx * ES, v, t, cols);
       ny[v] = R::fetch(static_cast<const char*>(p.dy) + row * p.lddy * ES, v, t, cols);
-      if (p.dsum) nd[v] = R::fetch(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols);
+      if (kAhead && p.dsum) nd[v] = R::fetch(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols);
     }
   };
-  constexpr bool kAhead = PER <= 2;   // beyond, there are no registers left for it
   int flip = 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * RG;
   if (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * RG + rg);
@@ -368,9 +290,9 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
     const float mean = nmean, rstd = nrstd;
 #pragma unroll
     for (int v = 0; v < PER; ++v) {
-      R::unpack(nx[v], x[v]);
-      R::unpack(ny[v], dy[v]);
-      ds[v] = nd[v];
+      unpack8<F32>(nx[v], x[v]);
+      unpack8<F32>(ny[v], dy[v]);
+      if (kAhead) ds[v] = nd[v];
     }
     if (kAhead) fetch(row + stride);
     if (live) {
@@ -392,7 +314,7 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
     for (int v = 0; v < PER; ++v) {
       float o[8], d[8];
       if (p.dsum) {
-        R::unpack(ds[v], d);
+        unpack8<F32>(kAhead ? ds[v] : R::fetch(static_cast<const char*>(p.dsum) + row * p.ldds * ES, v, t, cols), d);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] = 0.0f;
@@ -431,10 +353,7 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p, 
     }
     if (rg == 0) {
 #pragma unroll
-      for (int v = 0; v < PER; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (R::in(v, e, t, cols)) out[which * cols + R::col(v, e, t)] = acc[v][e];
+      for (int v = 0; v < PER; ++v) Row<true, NT>::store(out + which * cols, v, t, cols, acc[v]);
     }
   }
 }
@@ -543,12 +462,11 @@ int64_t bwd_partial_rows(int64_t rows, int64_t cols) {
   return blocks < kBwdBlocks ? blocks : kBwdBlocks;
 }
 
-template <bool F32, bool VEC>
+template <bool F32>
 hipError_t launch_bwd(const NormBwd& p, hipStream_t s) {
-  const bool gv = p.gamma && al16(p.gamma);
   const uint32_t grid = static_cast<uint32_t>(bwd_partial_rows(p.rows, p.cols));
   switch (bwd_nt(p.cols)) {
-#define DSMOE_LNB(NT, PER) layer_norm_bwd_kernel<F32, VEC, NT, PER><<<grid, kBwdThreads, 0, s>>>(p, gv)
+#define DSMOE_LNB(NT, PER) layer_norm_bwd_kernel<F32, NT, PER><<<grid, kBwdThreads, 0, s>>>(p)
     case 64: DSMOE_LNB(64, 2); break;
     case 128: DSMOE_LNB(128, 2); break;
     case 256: DSMOE_LNB(256, 2); break;
@@ -576,11 +494,7 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_layer_norm(const NormFwd& p, hipStream_t s) {
-  const int es = p.x_f32 ? 4 : 2;
-  const bool vec = p.cols % 8 == 0 && row16(p.x, p.ldx, es) && row16(p.residual, p.ldr, es) &&
-                   row16(p.y, p.ldy, es) && row16(p.sum, p.lds, es);
-  if (p.x_f32) return vec ? launch_fwd<true, true>(p, s) : launch_fwd<true, false>(p, s);
-  return vec ? launch_fwd<false, true>(p, s) : launch_fwd<false, false>(p, s);
+  return p.x_f32 ? launch_fwd<true>(p, s) : launch_fwd<false>(p, s);
 }
 
 size_t layer_norm_backward_partial_floats(int64_t rows, int64_t cols) {
@@ -589,11 +503,7 @@ size_t layer_norm_backward_partial_floats(int64_t rows, int64_t cols) {
 
 hipError_t launch_layer_norm_backward(const NormBwd& p, hipStream_t s) {
   if (p.rows > 0) {
-    const int es = p.x_f32 ? 4 : 2;
-    const bool vec = p.cols % 8 == 0 && row16(p.dy, p.lddy, es) && row16(p.x, p.ldx, es) &&
-                     row16(p.dsum, p.ldds, es) && row16(p.dx, p.lddx, es);
-    const hipError_t e = p.x_f32 ? (vec ? launch_bwd<true, true>(p, s) : launch_bwd<true, false>(p, s))
-                                 : (vec ? launch_bwd<false, true>(p, s) : launch_bwd<false, false>(p, s));
+    const hipError_t e = p.x_f32 ? launch_bwd<true>(p, s) : launch_bwd<false>(p, s);
     if (e != hipSuccess) return e;
   }
   if (!p.dgamma) return hipSuccess;
