@@ -805,10 +805,6 @@ struct Plan {
   double us;      // estimated time
 };
 
-bool row16(const void* p, int64_t ld, int es) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
-}
-
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -908,14 +904,16 @@ hipError_t launch_shape(const TileArgs& t, hipStream_t s) {
 
 // Whether the kernel for few tokens takes a product.  Its time is W's way from
 // memory or x's way from L2 to every block (about 35 KB per us and CU),
-// whichever is longer, and some of the other; unaligned rows are read value by
-// value.  4096 x 7168: 1 token 12 us (tiles 18), 16 tokens 16 (19), 32 tokens
-// 22 (19); 1000 x 1000: 64 tokens 6.5 (9).
+// whichever is longer, and some of the other; wide loads of rows off 4 bytes
+// take 2.3 times as long (7168 x 2047 17.8 us, 7168 x 2044 8.1).  4096 x 7168:
+// 1 token 12 us (tiles 18), 16 tokens 16 (19), 32 tokens 22 (19); 1000 x 1000:
+// 64 tokens 6.5 (9).
 bool few_tokens(const DenseGemm& p, const Plan& pl) {
   if (p.M > 64 || p.a.k_rows || p.b.k_rows) return false;
   const bool gated = p.epi == DenseEpi::kGated;
   const int64_t blocks = gated ? (p.N + 7) / 8 : (p.N + 15) / 16, groups = (p.M + 15) / 16;
-  const double slow = row16(p.a.p, p.a.ld, 2) && row16(p.b.p, p.b.ld, 2) ? 1.0 : 3.0;
+  auto even = [](const Operand& o) { return reinterpret_cast<uintptr_t>(o.p) % 4 == 0 && o.ld % 2 == 0; };
+  const double slow = even(p.a) && even(p.b) ? 1.0 : 2.3;
   const double w = slow * (gated ? 2.0 : 1.0) * p.N * p.K * 2 / kHbm;
   const double rounds = blocks > kCus ? static_cast<double>(blocks) / kCus : 1.0;
   const double x = p.M == 1 ? 0.0 : slow * rounds * groups * 16 * p.K * 2 / 35e3;
