@@ -1,7 +1,7 @@
 """The dense feed-forward sub-layer on one GPU: training steps (forward,
 backward, a plain update of float32 master weights) and single-token serving.
 
-    python examples/dense_ffn_step.py [--tokens 4096 --hidden 7168 --inner 2048 --steps 5]
+    python examples/dense_ffn_step.py [--tokens 4096 --hidden 7168 --inner 2048 --steps 5 --lr 0.01]
 """
 
 import argparse
@@ -22,6 +22,7 @@ def main():
     ap.add_argument("--hidden", type=int, default=7168)
     ap.add_argument("--inner", type=int, default=2048)
     ap.add_argument("--steps", type=int, default=5)
+    ap.add_argument("--lr", type=float, default=0.01)
     a = ap.parse_args()
     torch.manual_seed(0)
     T, H, I = a.tokens, a.hidden, a.inner
@@ -40,7 +41,7 @@ def main():
         dy = (y - target) * (2.0 / T)
         g = d.dense_ffn_backward(dy, saved, master["gamma"], w13, w2)
         for name in master:
-            master[name].sub_(g["d" + name], alpha=0.1)
+            master[name].sub_(g["d" + name], alpha=a.lr)
         w13.copy_(master["w13"])
         w2.copy_(master["w2"])
         torch.cuda.synchronize()

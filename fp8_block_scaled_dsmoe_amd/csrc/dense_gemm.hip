@@ -29,7 +29,6 @@
 #include "act.h"
 #include "common.h"
 #include "dense.h"
-#include "dense_epi.h"
 #include "vec8.h"
 
 namespace dsmoe {

@@ -14,15 +14,43 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act.h"
 #include "common.h"
 #include "dense.h"
-#include "dense_epi.h"
 #include "vec8.h"
 
 namespace dsmoe {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float load1(const void* p, int64_t i, bool f32) {
+  return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float v) {
+  if (f32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(f32x2_to_bf16x2(v, 0.0f));
+}
+
+// y = act(v + bias) + r, z = v + bias; r: the residual's value, if there is one
+__device__ __forceinline__ void finish_linear1(const DenseGemm& p, int64_t m, int64_t n, float v, float r) {
+  if (p.bias) v += load1(p.bias, n, p.bias_f32);
+  if (p.z) store1(p.z, m * p.ldz + n, p.y_f32, v);
+  v = act_f32(p.act, v);
+  if (p.residual) v += r;
+  store1(p.y, m * p.ldy + n, p.y_f32, v);
+}
+
+// a = act(g) u, h = [g | u]
+__device__ __forceinline__ void finish_gated1(const DenseGemm& p, int64_t m, int64_t n, float g, float u) {
+  if (p.z) {
+    store1(p.z, m * p.ldz + n, false, g);
+    store1(p.z, m * p.ldz + p.gate_n + n, false, u);
+  }
+  store1(p.y, m * p.ldy + n, p.y_f32, act_f32(p.act, g) * u);
+}
 
 __device__ __forceinline__ u32x4 load_frag(const uint16_t* q) { return *reinterpret_cast<const u32x4_at2*>(q); }
 
