@@ -100,7 +100,8 @@ BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool bias
     L.dz = c.take(static_cast<size_t>(M) * L.lddz * 2);
     dy = nullptr;   // the workspace's own rows are aligned
   }
-  if (bias) L.partial = c.take(static_cast<size_t>(dsmoe::bias_partial_rows(M, N)) * N * 4);
+  if (bias && dsmoe::bias_partial_rows(M, N) > 1)
+    L.partial = c.take(static_cast<size_t>(dsmoe::bias_partial_rows(M, N)) * N * 4);
   const size_t a = dsmoe::dense_gemm_workspace_bytes(dx_product(dy, L.lddz, own_dz, w, ldw, M, N, K));
   const size_t b = dsmoe::dense_gemm_workspace_bytes(dw_product(dy, L.lddz, own_dz, x, ldx, M, N, K));
   L.product = c.take(a > b ? a : b);
@@ -261,10 +262,10 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
     }
   } else if (dbias || L.own_dz) {
     uint16_t* to = L.own_dz && (dx || dw) ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
-    float* partial = dbias ? reinterpret_cast<float*>(base + L.partial) : nullptr;
+    const int64_t strips = dsmoe::bias_partial_rows(M, N);
+    float* partial = dbias && strips > 1 ? reinterpret_cast<float*>(base + L.partial) : dbias;
     hipError_t e = dsmoe::launch_act_backward(dz, lddy, z, ldz, zt == DSMOE_F32, act, M, N, to, L.lddz, partial, st);
-    if (e == hipSuccess && dbias)
-      e = dsmoe::launch_sum_partials(partial, dsmoe::bias_partial_rows(M, N), N, dbias, st);
+    if (e == hipSuccess && partial != dbias) e = dsmoe::launch_sum_partials(partial, strips, N, dbias, st);
     if (e != hipSuccess) return launch_status(e);
     if (to) dz = to;
   }

@@ -104,7 +104,8 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __r
 constexpr int64_t kMaxBlocks = 1 << 23;   // 2^31 threads; a launch holds fewer than 2^32
 
 // column slots of a block of act_backward_kernel, rows of a strip: about 1024
-// blocks, of at least two steps of rows each
+// blocks, of at least two steps of rows each; few rows are one strip, whose
+// sums need no second launch
 int column_slots(int64_t N) {
   int ct = 1;
   while (ct < 32 && ct * 8 < N) ct *= 2;
@@ -115,6 +116,7 @@ int64_t strip_rows(int64_t M, int64_t N) {
   const int64_t blocks_n = (N + 8 * ct - 1) / (8 * ct), step = 256 / ct;
   const int64_t strips = (1024 + blocks_n - 1) / blocks_n, least = (M + 65534) / 65535;   // the grid's limit
   const int64_t rows = (M + strips - 1) / strips;
+  if (M <= 4 * step) return M;
   const int64_t s = rows < 2 * step ? 2 * step : rows;
   return s < least ? least : s;
 }
