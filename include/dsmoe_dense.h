@@ -14,8 +14,9 @@
  * validation before anything is enqueued, status codes), except that:
  * - Matrices are row-major with a row stride in elements (ld..., at least the
  *   row length); columns are contiguous.  Any size and any element-aligned
- *   pointer is accepted.  Operands whose rows are not 16-byte aligned or
- *   whose length is not a multiple of 8 are copied into the workspace first.
+ *   pointer is accepted.  Operands of products whose rows are not 16-byte
+ *   aligned or whose length is not a multiple of 8 may be copied into the
+ *   workspace first.
  * - NaN and infinities propagate as in the formulas.
  * - Sizes: every row length and row stride is in [1, DSMOE_DENSE_MAX_DIM];
  *   rows / tokens in [0, 2^31).  No rows: outputs per row are not touched,
