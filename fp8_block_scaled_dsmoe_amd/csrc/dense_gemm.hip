@@ -112,9 +112,12 @@ __device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* 
 // Asynchronous copy of 16 bytes per lane to lds + 16 lane (wave-uniform lds):
 // offset voff from the resource's base; past its range zeros are written.
 // Issued from assembly so that the compiler neither waits for it nor counts
-// it; the kernel waits for vmcnt itself.
+// it; the kernel waits for vmcnt itself.  A copy to LDS must not follow a
+// write of M0 directly (one wait state, which the compiler cannot add inside
+// assembly).
 __device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(lds)
                : "memory", "m0");
 }
 template <int N>

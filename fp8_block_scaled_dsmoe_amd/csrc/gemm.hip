@@ -419,13 +419,15 @@ struct LdsCfg {
 // lands asynchronously and is counted by vmcnt like any vector load; these
 // copies are issued from inline assembly so that the compiler neither waits
 // for them conservatively nor counts them, and the kernel waits for them
-// explicitly (vector memory operations of a wave complete in order).
+// explicitly (vector memory operations of a wave complete in order).  A copy
+// must not follow a write of M0 directly: the one wait state that takes is
+// the s_nop, as the compiler adds none inside assembly.
 __device__ __forceinline__ void dma_16(const void* g, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_base)
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds_base)
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma_4(const void* g, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_base)
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_base)
                : "memory", "m0");
 }
 // The same copy through a buffer resource (base and range in SGPRs): the
@@ -444,12 +446,12 @@ __device__ __forceinline__ i32x4_rsrc buffer_rsrc(const void* base) {
 }
 __device__ __forceinline__ void dma_16_buf(const i32x4_rsrc& rsrc, uint32_t voff, uint32_t soff,
                                            uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(voff), "s"(rsrc),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(voff), "s"(rsrc),
                "s"(lds_base), "s"(soff)
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma_4_buf(const i32x4_rsrc& rsrc, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
                "s"(lds_base)
                : "memory", "m0");
 }
