@@ -39,7 +39,9 @@ def main():
         t0 = time.perf_counter()
         y, saved = d.dense_ffn_forward(x, master["gamma"], master["beta"], w13, w2, training=True)
         dy = (y - target) * (2.0 / T)
-        g = d.dense_ffn_backward(dy, saved, master["gamma"], w13, w2)
+        # every product on bf16 operands; without dz_dtype the float32 gradient
+        # of w13 would take a second product for the rest of its operand
+        g = d.dense_ffn_backward(dy, saved, master["gamma"], w13, w2, dz_dtype=torch.bfloat16)
         for name in master:
             master[name].sub_(g["d" + name], alpha=a.lr)
         w13.copy_(master["w13"])

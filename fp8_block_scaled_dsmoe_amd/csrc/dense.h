@@ -99,14 +99,17 @@ hipError_t launch_dense_skinny(const DenseGemm& p, hipStream_t s);
 hipError_t launch_zero_matrix(void* dst, int64_t ldd, bool f32, int64_t m, int64_t n, hipStream_t s);
 
 // dense_grad.hip -------------------------------------------------------------
-// dz = dy * act'(z) as bf16 [M][lddz] (dz null: not wanted) and its column
-// sums over each of bias_partial_rows() strips of rows, partial [strips][N]
-// (null: not wanted); z null: act' = 1
+// dz = dy * act'(z) as bf16 [M][lddz] (dz null: not wanted), what that rounding
+// leaves of it as bf16 in dz_lo (null: not wanted), and its column sums over
+// each of bias_partial_rows() strips of rows, partial [strips][N] (null: not
+// wanted); z null: act' = 1
 int64_t bias_partial_rows(int64_t M, int64_t N);
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz, bool z_f32, int act,
-                               int64_t M, int64_t N, uint16_t* dz, int64_t lddz, float* partial, hipStream_t s);
-// dh = [da u act'(g) | da act(g)] as bf16 [M][lddh] from h = [g | u]
+                               int64_t M, int64_t N, uint16_t* dz, uint16_t* dz_lo, int64_t lddz, float* partial,
+                               hipStream_t s);
+// dh = [da u act'(g) | da act(g)] as bf16 [M][lddh] from h = [g | u], and in
+// dh_lo as above
 hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_t* h, int64_t ldh, int act,
-                                 int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s);
+                                 int64_t M, int64_t I, uint16_t* dh, uint16_t* dh_lo, int64_t lddh, hipStream_t s);
 
 }  // namespace dsmoe

@@ -29,6 +29,8 @@ bool half_dim_ok(int64_t n) { return n >= 1 && n <= DSMOE_DENSE_MAX_DIM / 2; }
 bool ld_ok(const void* p, int64_t ld, int64_t cols) { return !p || (ld >= cols && ld <= DSMOE_DENSE_MAX_DIM); }
 bool el_aligned(const void* p, int t) { return !p || aligned(p, esize(t)); }
 bool act_ok(int act) { return act >= DSMOE_ACT_NONE && act <= DSMOE_ACT_RELU; }
+// act of a backward call
+bool grad_act_ok(int act) { return act_ok(act & ~DSMOE_DZ_BF16); }
 Operand operand(const void* p, int64_t ld, bool k_rows, bool padded = false) {
   return Operand{static_cast<const uint16_t*>(p), ld, k_rows, padded};
 }
@@ -80,16 +82,16 @@ void set_output(DenseGemm& g, void* y, int64_t ldy, int yt) {
   g.y_f32 = yt == DSMOE_F32;
 }
 
-// Workspace of the two products of a backward pass, whose dz has N columns:
-// dz (when it is not dy itself: an activation, or rows the products cannot
-// copy), the bias partials, one product's scratch (the two run one after the
-// other).
+// Workspace of the products of a backward pass, whose dz has N columns: dz
+// (when it is not dy itself: an activation, or rows the products cannot copy),
+// where `two` what its rounding to bf16 leaves, the bias partials, one
+// product's scratch (they run one after the other).
 struct BackwardLayout {
-  size_t dz, partial, product, total;
+  size_t dz, dz_lo, partial, product, total;
   int64_t lddz;
   bool own_dz;
 };
-BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool bias, const void* x, int64_t ldx,
+BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool two, bool bias, const void* x, int64_t ldx,
                                const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K) {
   BackwardLayout L{};
   if (M == 0) return L;
@@ -98,6 +100,7 @@ BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool bias
   L.lddz = own_dz ? (N + 7) / 8 * 8 : lddy;
   if (own_dz) {
     L.dz = c.take(static_cast<size_t>(M) * L.lddz * 2);
+    if (two) L.dz_lo = c.take(static_cast<size_t>(M) * L.lddz * 2);
     dy = nullptr;   // the workspace's own rows are aligned
   }
   if (bias && dsmoe::bias_partial_rows(M, N) > 1)
@@ -109,26 +112,30 @@ BackwardLayout backward_layout(const void* dy, int64_t lddy, bool act, bool bias
   return L;
 }
 
-// dx and dw from dz; M = 0 leaves dx alone and clears dw
-dsmoe_status run_products(const void* dz, int64_t lddz, bool padded, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                          int64_t M, int64_t N, int64_t K, void* dx, int64_t lddx, int dxt, void* dw, int64_t lddw,
-                          int dwt, void* scratch, hipStream_t st) {
+// dx and dw from dz; M = 0 leaves dx alone and clears dw.  dz_lo: what dz's
+// rounding left of it, or null; a float32 gradient adds its product.
+dsmoe_status run_products(const void* dz, const void* dz_lo, int64_t lddz, bool padded, const void* x, int64_t ldx,
+                          const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K, void* dx, int64_t lddx, int dxt,
+                          void* dw, int64_t lddw, int dwt, void* scratch, hipStream_t st) {
   if (M == 0) return dw ? launch_status(dsmoe::launch_zero_matrix(dw, lddw, dwt == DSMOE_F32, N, K, st)) : DSMOE_OK;
-  if (dx) {
-    DenseGemm g = dx_product(dz, lddz, padded, w, ldw, M, N, K);
-    set_output(g, dx, lddx, dxt);
+  auto gradient = [&](DenseGemm g, void* y, int64_t ldy, int yt) {
+    set_output(g, y, ldy, yt);
     g.workspace = scratch;
     const hipError_t e = dsmoe::launch_dense_gemm(g, st);
-    if (e != hipSuccess) return launch_status(e);
-  }
-  if (dw) {
-    DenseGemm g = dw_product(dz, lddz, padded, x, ldx, M, N, K);
-    set_output(g, dw, lddw, dwt);
-    g.workspace = scratch;
-    const hipError_t e = dsmoe::launch_dense_gemm(g, st);
-    if (e != hipSuccess) return launch_status(e);
-  }
-  return DSMOE_OK;
+    if (e != hipSuccess || yt != DSMOE_F32 || !dz_lo) return e;
+    g.a.p = static_cast<const uint16_t*>(dz_lo);
+    g.residual = y, g.ldr = ldy;
+    return dsmoe::launch_dense_gemm(g, st);
+  };
+  hipError_t e = hipSuccess;
+  if (dx) e = gradient(dx_product(dz, lddz, padded, w, ldw, M, N, K), dx, lddx, dxt);
+  if (e == hipSuccess && dw) e = gradient(dw_product(dz, lddz, padded, x, ldx, M, N, K), dw, lddw, dwt);
+  return launch_status(e);
+}
+
+// Whether a float32 gradient is wanted, whose dz keeps what its rounding leaves.
+bool f32_gradient(const void* dx, int dxt, const void* dw, int dwt) {
+  return (dx && dxt == DSMOE_F32) || (dw && dwt == DSMOE_F32);
 }
 
 }  // namespace
@@ -223,8 +230,9 @@ dsmoe_status dsmoe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
 size_t dsmoe_linear_backward_workspace_bytes(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                              const void* w, int64_t ldw, int act, int64_t M, int64_t N,
                                              int64_t K) {
-  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act) || M == 0) return 0;
-  return backward_layout(dy, lddy, act != DSMOE_ACT_NONE, true, x, ldx, w, ldw, M, N, K).total;
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !grad_act_ok(act) || M == 0) return 0;
+  const bool has_act = (act & ~DSMOE_DZ_BF16) != DSMOE_ACT_NONE;
+  return backward_layout(dy, lddy, has_act, has_act && !(act & DSMOE_DZ_BF16), true, x, ldx, w, ldw, M, N, K).total;
 }
 
 dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
@@ -233,8 +241,10 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
                                    int64_t lddw, int dwt, float* dbias, void* workspace, size_t ws_bytes,
                                    void* stream) {
   if (!valid_dtype(zt) || !valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
-  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !act_ok(act)) return DSMOE_ERR_SHAPE;
-  const bool has_act = act != DSMOE_ACT_NONE;
+  if (!rows_ok(M) || !dim_ok(N) || !dim_ok(K) || !grad_act_ok(act)) return DSMOE_ERR_SHAPE;
+  const bool bf16_dz = act & DSMOE_DZ_BF16;
+  act &= ~DSMOE_DZ_BF16;
+  const bool has_act = act != DSMOE_ACT_NONE, two = has_act && !bf16_dz;
   if (!has_act) z = nullptr;
   if (!ld_ok(dy, lddy, N) || !ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(z, ldz, N) || !ld_ok(dx, lddx, K) ||
       !ld_ok(dw, lddw, K))
@@ -245,7 +255,7 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
     return DSMOE_ERR_ALIGN;
   if (!dx && !dw && !dbias) return DSMOE_OK;
   if (M == 0 && !dw && !dbias) return DSMOE_OK;
-  const BackwardLayout L = backward_layout(dy, lddy, has_act, true, x, ldx, w, ldw, M, N, K);
+  const BackwardLayout L = backward_layout(dy, lddy, has_act, two, true, x, ldx, w, ldw, M, N, K);
   if (M > 0) {
     const dsmoe_status ws = check_workspace(workspace, ws_bytes, L.total);
     if (ws != DSMOE_OK) return ws;
@@ -255,6 +265,7 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
   const hipStream_t st = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const uint16_t* dz = static_cast<const uint16_t*>(dy);
+  uint16_t* lo = two && f32_gradient(dx, dxt, dw, dwt) ? reinterpret_cast<uint16_t*>(base + L.dz_lo) : nullptr;
   if (M == 0) {
     if (dbias) {
       const hipError_t e = dsmoe::launch_zero_matrix(dbias, N, true, 1, N, st);
@@ -264,12 +275,13 @@ dsmoe_status dsmoe_linear_backward(const void* dy, int64_t lddy, const void* x, 
     uint16_t* to = L.own_dz && (dx || dw) ? reinterpret_cast<uint16_t*>(base + L.dz) : nullptr;
     const int64_t strips = dsmoe::bias_partial_rows(M, N);
     float* partial = dbias && strips > 1 ? reinterpret_cast<float*>(base + L.partial) : dbias;
-    hipError_t e = dsmoe::launch_act_backward(dz, lddy, z, ldz, zt == DSMOE_F32, act, M, N, to, L.lddz, partial, st);
+    hipError_t e = dsmoe::launch_act_backward(dz, lddy, z, ldz, zt == DSMOE_F32, act, M, N, to, lo, L.lddz, partial, st);
     if (e == hipSuccess && partial != dbias) e = dsmoe::launch_sum_partials(partial, strips, N, dbias, st);
     if (e != hipSuccess) return launch_status(e);
     if (to) dz = to;
   }
-  return run_products(dz, L.lddz, L.own_dz, x, ldx, w, ldw, M, N, K, dx, lddx, dxt, dw, lddw, dwt, base + L.product, st);
+  return run_products(dz, lo, L.lddz, L.own_dz, x, ldx, w, ldw, M, N, K, dx, lddx, dxt, dw, lddw, dwt, base + L.product,
+                      st);
 }
 
 size_t dsmoe_gated_linear_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw, int64_t M,
@@ -302,7 +314,7 @@ dsmoe_status dsmoe_gated_linear(const void* x, int64_t ldx, const void* w13, int
 size_t dsmoe_gated_linear_backward_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw,
                                                    int64_t M, int64_t H, int64_t I) {
   if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || M == 0) return 0;
-  return backward_layout(nullptr, 0, true, false, x, ldx, w13, ldw, M, 2 * I, H).total;
+  return backward_layout(nullptr, 0, true, true, false, x, ldx, w13, ldw, M, 2 * I, H).total;
 }
 
 dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const void* x, int64_t ldx,
@@ -311,7 +323,9 @@ dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const voi
                                          void* dw13, int64_t lddw, int dwt, void* workspace, size_t ws_bytes,
                                          void* stream) {
   if (!valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
-  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || !act_ok(act)) return DSMOE_ERR_SHAPE;
+  if (!rows_ok(M) || !dim_ok(H) || !half_dim_ok(I) || !grad_act_ok(act)) return DSMOE_ERR_SHAPE;
+  const bool two = !(act & DSMOE_DZ_BF16);
+  act &= ~DSMOE_DZ_BF16;
   if (!ld_ok(da, ldda, I) || !ld_ok(x, ldx, H) || !ld_ok(w13, ldw, H) || !ld_ok(h, ldh, 2 * I) ||
       !ld_ok(dx, lddx, H) || !ld_ok(dw13, lddw, H))
     return DSMOE_ERR_SHAPE;
@@ -320,7 +334,7 @@ dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const voi
       !el_aligned(dw13, dwt))
     return DSMOE_ERR_ALIGN;
   if ((!dx && !dw13) || (M == 0 && !dw13)) return DSMOE_OK;
-  const BackwardLayout L = backward_layout(nullptr, 0, true, false, x, ldx, w13, ldw, M, 2 * I, H);
+  const BackwardLayout L = backward_layout(nullptr, 0, true, two, false, x, ldx, w13, ldw, M, 2 * I, H);
   if (M > 0) {
     const dsmoe_status ws = check_workspace(workspace, ws_bytes, L.total);
     if (ws != DSMOE_OK) return ws;
@@ -330,10 +344,12 @@ dsmoe_status dsmoe_gated_linear_backward(const void* da, int64_t ldda, const voi
   const hipStream_t st = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   uint16_t* dh = reinterpret_cast<uint16_t*>(base + L.dz);
+  uint16_t* lo = two && f32_gradient(dx, dxt, dw13, dwt) ? reinterpret_cast<uint16_t*>(base + L.dz_lo) : nullptr;
   const hipError_t e = dsmoe::launch_gated_backward(static_cast<const uint16_t*>(da), ldda,
-                                                    static_cast<const uint16_t*>(h), ldh, act, M, I, dh, L.lddz, st);
+                                                    static_cast<const uint16_t*>(h), ldh, act, M, I, dh, lo, L.lddz, st);
   if (e != hipSuccess) return launch_status(e);
-  return run_products(dh, L.lddz, true, x, ldx, w13, ldw, M, 2 * I, H, dx, lddx, dxt, dw13, lddw, dwt, base + L.product, st);
+  return run_products(dh, lo, L.lddz, true, x, ldx, w13, ldw, M, 2 * I, H, dx, lddx, dxt, dw13, lddw, dwt,
+                      base + L.product, st);
 }
 
 }  // extern "C"

@@ -1,6 +1,9 @@
 // Elementwise parts of the dense backward passes: the gradient at the
-// pre-activations, rounded to bf16 once as the operand of the two products
-// that follow, and the bias gradient's column sums (of the unrounded values).
+// pre-activations, as the operand of the two products that follow, and the
+// bias gradient's column sums (of the unrounded values).  The matrix cores take
+// bf16: the gradient is rounded to it once, as its products' bf16 results
+// are, and for float32 results the rounding's rest is kept as a second bf16
+// operand, 16 significant bits in all.
 // HBM bounds them: dy and z (or da and h) in, dz (dh) out.  Column sums alone of
 // 4096 x 7168 (58 MB): 13 us; the gated gradient of 4096 x 2 x 2048 (84 MB in
 // all): 21 us.
@@ -22,8 +25,8 @@ template <bool ZF32>
 __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                                            const void* __restrict__ z, int64_t ldz, int act,
                                                            int64_t M, int64_t N, int ct, int64_t strip,
-                                                           uint16_t* __restrict__ dz, int64_t lddz,
-                                                           float* __restrict__ partial) {
+                                                           uint16_t* __restrict__ dz, uint16_t* __restrict__ dz_lo,
+                                                           int64_t lddz, float* __restrict__ partial) {
   __shared__ float s_sum[256 * 8];
   const int slot = threadIdx.x % ct, rt = 256 / ct;
   const int64_t c = 8 * (static_cast<int64_t>(blockIdx.x) * ct + slot);
@@ -52,7 +55,12 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (c + e >= N) g[e] = 0.0f;
-        *reinterpret_cast<u32x4*>(dz + r * lddz + c) = pack8(g);
+        const u32x4 q = pack8(g);
+        *reinterpret_cast<u32x4*>(dz + r * lddz + c) = q;
+        if (dz_lo) {
+          rest8(g, q);
+          *reinterpret_cast<u32x4*>(dz_lo + r * lddz + c) = pack8(g);
+        }
       }
     }
   }
@@ -74,7 +82,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
 __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __restrict__ da, int64_t ldda,
                                                              const uint16_t* __restrict__ h, int64_t ldh, int act,
                                                              int64_t M, int64_t I,
-                                                             uint16_t* __restrict__ dh, int64_t lddh) {
+                                                             uint16_t* __restrict__ dh,
+                                                             uint16_t* __restrict__ dh_lo, int64_t lddh) {
   const uint32_t slots = static_cast<uint32_t>((I + 7) / 8);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < M * slots;
        i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -92,12 +101,20 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const uint16_t* __r
       dg[e] = d[e] * u[e] * df;
       du[e] = d[e] * f;
     }
-    uint16_t* o = dh + r * lddh + c;
-    put8<false>(o, I - c, dg);
-    put8<false>(o + I, I - c, du);
-    // the row's padding past 2 I, by the thread that owns the last column
-    if (c + 8 >= I)
-      for (int64_t j = 2 * I; j < lddh; ++j) dh[r * lddh + j] = 0;
+    auto store = [&](uint16_t* to) {
+      uint16_t* o = to + r * lddh + c;
+      put8<false>(o, I - c, dg);
+      put8<false>(o + I, I - c, du);
+      // the row's padding past 2 I, by the thread that owns the last column
+      if (c + 8 >= I)
+        for (int64_t j = 2 * I; j < lddh; ++j) to[r * lddh + j] = 0;
+    };
+    store(dh);
+    if (dh_lo) {
+      rest8(dg, pack8(dg));
+      rest8(du, pack8(du));
+      store(dh_lo);
+    }
   }
 }
 
@@ -128,24 +145,25 @@ int64_t bias_partial_rows(int64_t M, int64_t N) {
 }
 
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz, bool z_f32, int act,
-                               int64_t M, int64_t N, uint16_t* dz, int64_t lddz, float* partial, hipStream_t s) {
+                               int64_t M, int64_t N, uint16_t* dz, uint16_t* dz_lo, int64_t lddz, float* partial,
+                               hipStream_t s) {
   if (M == 0) return hipSuccess;
   const int ct = column_slots(N);
   const int64_t strip = strip_rows(M, N);
   const dim3 grid(static_cast<uint32_t>((N + 8 * ct - 1) / (8 * ct)), static_cast<uint32_t>((M + strip - 1) / strip));
   if (z_f32)
-    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, lddz, partial);
+    act_backward_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, dz_lo, lddz, partial);
   else
-    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, lddz, partial);
+    act_backward_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, act, M, N, ct, strip, dz, dz_lo, lddz, partial);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_backward(const uint16_t* da, int64_t ldda, const uint16_t* h, int64_t ldh, int act,
-                                 int64_t M, int64_t I, uint16_t* dh, int64_t lddh, hipStream_t s) {
+                                 int64_t M, int64_t I, uint16_t* dh, uint16_t* dh_lo, int64_t lddh, hipStream_t s) {
   if (M == 0) return hipSuccess;
   const int64_t all = (M * ((I + 7) / 8) + 255) / 256;
   const uint32_t blocks = static_cast<uint32_t>(all < kMaxBlocks ? all : kMaxBlocks);
-  gated_backward_kernel<<<blocks, 256, 0, s>>>(da, ldda, h, ldh, act, M, I, dh, lddh);
+  gated_backward_kernel<<<blocks, 256, 0, s>>>(da, ldda, h, ldh, act, M, I, dh, dh_lo, lddh);
   return hipGetLastError();
 }
 

@@ -101,6 +101,15 @@ __device__ __forceinline__ void put8(void* p, int64_t left, const float* v) {
   }
 }
 
+// v less its bf16 rounding q, 0 where q is not finite (infinity less infinity
+// would be NaN)
+__device__ __forceinline__ void rest8(float* v, const u32x4& q) {
+  float r[8];
+  unpack8<false>(Raw8<false>{{q}}, r);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __builtin_isfinite(r[e]) ? v[e] - r[e] : 0.0f;
+}
+
 // The same for values i, i + 1, ... of a matrix or vector whose type is known
 // at run time.
 __device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, int64_t left, float* o) {

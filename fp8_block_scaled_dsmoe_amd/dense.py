@@ -22,6 +22,8 @@ __all__ = ["ACTIVATIONS", "layer_norm", "layer_norm_backward", "linear", "linear
 
 # dsmoe_act codes
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+# DSMOE_DZ_BF16
+_DZ_BF16 = 16
 
 _vp, _i64, _int, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _MAT = [_vp, _i64]
@@ -143,6 +145,13 @@ def _act(act):
     return ACTIVATIONS[act]
 
 
+def _grad_act(act, dz_dtype):
+    """The act code of a backward call."""
+    if dz_dtype not in (None, torch.bfloat16):
+        raise TypeError("dz_dtype must be None or torch.bfloat16")
+    return _act(act) | (0 if dz_dtype is None else _DZ_BF16)
+
+
 def _scratch(workspace, need, device):
     """(tensor to keep alive, pointer, bytes) of the workspace of a call."""
     if workspace is None:
@@ -252,24 +261,29 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     return y, z
 
 
-def linear_backward_workspace_bytes(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none") -> int:
+def linear_backward_workspace_bytes(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none",
+                                    dz_dtype: Optional[torch.dtype] = None) -> int:
     """Workspace of linear_backward on these operands (their sizes and alignment)."""
     (dp, ldd), (xp, ldx), (wp, ldw) = (_mat(dy, None, torch.bfloat16, "dy"), _mat(x, None, torch.bfloat16, "x"),
                                        _mat(w, None, torch.bfloat16, "w"))
-    return int(lib.dsmoe_linear_backward_workspace_bytes(dp, ldd, xp, ldx, wp, ldw, _act(act), dy.shape[0],
-                                                         dy.shape[1], w.shape[1]))
+    return int(lib.dsmoe_linear_backward_workspace_bytes(dp, ldd, xp, ldx, wp, ldw, _grad_act(act, dz_dtype),
+                                                         dy.shape[0], dy.shape[1], w.shape[1]))
 
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: Optional[torch.Tensor] = None,
                     act: str = "none", dx_dtype=torch.bfloat16, dw_dtype=torch.float32, need_dx: bool = True,
                     need_dw: bool = True, need_dbias: bool = False, dx: Optional[torch.Tensor] = None,
-                    dw: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                    dw: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    dz_dtype: Optional[torch.dtype] = None):
     """Gradients of linear (dsmoe_linear_backward).  dy bf16 [M][N]; x, w the
     forward's; z the saved pre-activation (bf16 or f32), needed unless act is
-    "none".  The residual's gradient is dy.  Returns (dx [M][K], dw [N][K],
-    dbias f32 [N]), None where not wanted."""
+    "none".  The residual's gradient is dy.  With an activation, float32
+    gradients keep 16 bits of dz = dy act'(z) at twice a product's time;
+    dz_dtype torch.bfloat16 rounds it to bf16 for them too, as for bf16
+    gradients.  Returns (dx [M][K], dw [N][K], dbias f32 [N]), None where not
+    wanted."""
     device, stream = _begin(dy, "dy")
-    code = _act(act)
+    code = _grad_act(act, dz_dtype)
     dyp, lddy = _mat(dy, None, torch.bfloat16, "dy")
     M, N = dy.shape
     wp, ldw = _mat(w, None, torch.bfloat16, "w", device)
@@ -279,7 +293,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: Optio
     xp, ldx = _mat(x, (M, K), torch.bfloat16, "x", device)
     zp, ldz = _mat(z, (M, N), None, "z", device)
     zt = BF16 if z is None else _dtype_code(z.dtype)
-    if code and z is None:
+    if act != "none" and z is None:
         raise ValueError(f"act {act!r} needs the saved z")
     dxp, lddx, dxt, dwp, lddw, dwt = None, 0, BF16, None, 0, F32
     if dx is not None or need_dx:
@@ -339,12 +353,14 @@ def gated_linear_backward_workspace_bytes(x: torch.Tensor, w13: torch.Tensor) ->
 def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, h: torch.Tensor, act: str = "silu",
                           dx_dtype=torch.bfloat16, dw_dtype=torch.float32, need_dx: bool = True,
                           need_dw: bool = True, dx: Optional[torch.Tensor] = None,
-                          dw13: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                          dw13: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          dz_dtype: Optional[torch.dtype] = None):
     """Gradients of gated_linear (dsmoe_gated_linear_backward) from the saved
-    h.  da bf16 [M][I].  Returns (dx [M][H], dw13 [2I][H]), None where not
-    wanted."""
+    h.  da bf16 [M][I].  Float32 gradients keep 16 bits of the gradient at h, at
+    twice a product's time; dz_dtype as in linear_backward.  Returns (dx
+    [M][H], dw13 [2I][H]), None where not wanted."""
     device, stream = _begin(da, "da")
-    code = _act(act)
+    code = _grad_act(act, dz_dtype)
     dap, ldda = _mat(da, None, torch.bfloat16, "da")
     M, I = da.shape
     wp, ldw = _mat(w13, None, torch.bfloat16, "w13", device)
@@ -386,11 +402,12 @@ def dense_ffn_forward(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opti
 
 
 def dense_ffn_backward(dy: torch.Tensor, saved: dict, gamma: Optional[torch.Tensor], w13: torch.Tensor,
-                       w2: torch.Tensor, act: str = "silu", dw_dtype=torch.float32):
-    """Gradients of dense_ffn_forward from dy bf16 [T][H] and its saved dict.
-    Returns {"dx" (of x and of residual alike), "dgamma", "dbeta", "dw13",
-    "dw2"}."""
+                       w2: torch.Tensor, act: str = "silu", dw_dtype=torch.float32,
+                       dz_dtype: Optional[torch.dtype] = None):
+    """Gradients of dense_ffn_forward from dy bf16 [T][H] and its saved dict;
+    dz_dtype as in gated_linear_backward.  Returns {"dx" (of x and of residual
+    alike), "dgamma", "dbeta", "dw13", "dw2"}."""
     da, dw2, _ = linear_backward(dy, saved["a"], w2, dw_dtype=dw_dtype)
-    dn, dw13 = gated_linear_backward(da, saved["n"], w13, saved["h"], act, dw_dtype=dw_dtype)
+    dn, dw13 = gated_linear_backward(da, saved["n"], w13, saved["h"], act, dw_dtype=dw_dtype, dz_dtype=dz_dtype)
     dx, dgamma, dbeta = layer_norm_backward(dn, saved["s"], saved["mean"], saved["rstd"], gamma, dsum=dy)
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta, "dw13": dw13, "dw2": dw2}

@@ -109,10 +109,13 @@ dsmoe_status dsmoe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
  *   dx     [M][K], type dxt, or NULL
  *   dw     [N][K], type dwt, or NULL
  *   dbias  [N] f32, or NULL
- * With an activation dz is rounded to bf16 once, as the operand of both
- * products (dbias sums it unrounded); without one dz is dy and the products
- * are exact.
+ * Without an activation dz is dy and its products are exact.  With one dz is
+ * formed in float32 (and dbias sums it so).  It enters a bf16 gradient rounded
+ * to bf16, and a float32 gradient as the sum of two bf16 values, which keeps
+ * 16 significant bits and takes a product for each.  With act |
+ * DSMOE_DZ_BF16 it is rounded to bf16 for float32 gradients too.
  */
+#define DSMOE_DZ_BF16 16
 size_t dsmoe_linear_backward_workspace_bytes(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                                              const void* w, int64_t ldw, int act, int64_t M, int64_t N,
                                              int64_t K);
@@ -144,8 +147,8 @@ dsmoe_status dsmoe_gated_linear(const void* x, int64_t ldx, const void* w13, int
  *   x     [M][H], w13 [2I][H], h [M][2I] bf16: the forward's
  *   dx    [M][H], type dxt, or NULL
  *   dw13  [2I][H], type dwt, or NULL
- * dh is formed in float32 and rounded to bf16 once, as the operand of both
- * products.
+ * dh is formed in float32 and enters the products as dz in
+ * dsmoe_linear_backward, act | DSMOE_DZ_BF16 included.
  */
 size_t dsmoe_gated_linear_backward_workspace_bytes(const void* x, int64_t ldx, const void* w13, int64_t ldw,
                                                    int64_t M, int64_t H, int64_t I);

@@ -162,6 +162,21 @@ def test_gated_linear_backward_refusals(d):
     assert _gated_bwd(d, M=0, dw=None) == OK
 
 
+def test_backward_calls_take_the_bf16_dz_flag_and_no_other(d):
+    flag = 16
+    args = (A, 32, A, 64, A, 64)
+    size = d.lib.dsmoe_linear_backward_workspace_bytes
+    # dz of an activation keeps the rest of its rounding unless told not to
+    assert size(*args, 1, 128, 32, 64) - size(*args, 1 | flag, 128, 32, 64) == 128 * 32 * 2
+    assert size(*args, 0, 128, 32, 64) == size(*args, flag, 128, 32, 64)
+    for call in (_linear_bwd, _gated_bwd):
+        assert call(d, act=3 | flag, ws=None) == WORKSPACE
+        assert call(d, act=4 | flag) == SHAPE and call(d, act=2 * flag) == SHAPE and call(d, act=3 * flag) == SHAPE
+    assert _linear(d, act=1 | flag) == SHAPE and _gated(d, act=1 | flag) == SHAPE
+    need = size(*args, 1 | flag, 4, 32, 64)
+    assert _linear_bwd(d, act=1 | flag, wsn=need - 1) == WORKSPACE
+
+
 def test_python_refusals(d):
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):

@@ -635,3 +635,86 @@ def test_linear_tile_shapes(d, M, N, K):
         _linear_check(y[rm], z[rm], x64[rm], w64, b64, kind, res64, out, f"{kind} {out}")
         y2, _ = d.linear(x, w, bias, kind, res, DT[out])
         assert torch.equal(y, y2)
+
+
+# ---------------------------------------------------------------------------
+# float32 gradients where dz is formed
+# ---------------------------------------------------------------------------
+
+def _split_check(got, p, q, what):
+    """A float32 product of formed dz: two bf16 terms leave at most v^2 of a
+    value, each term independently, beside the float32 roundings of dz (2^-19)."""
+    bound = 16 * U * _norms(p, q.T) + (4 * V * V + 2.0 ** -19) * np.sqrt((p * p) @ (q * q))
+    _close(got, p @ q, bound, "f32", what)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 7, 3), (33, 257, 128), (65, 300, 515), (513, 768, 320), (3000, 130, 72)])
+def test_float32_gradients_of_an_activation(d, M, N, K):
+    r = np.random.default_rng(M + N)
+    x, x64 = _mat(r, M, K)
+    w, w64 = _mat(r, N, K, 0.1)
+    dy, dy64 = _mat(r, M, N, 0.1)
+    for kind in ("silu", "gelu"):
+        banner(f"float32 gradients of {kind}, {M}x{N}x{K}")
+        z, z64 = _mat(r, M, N, 1.5)
+        dz = od.linear_backward(dy64, x64, w64, z64, kind)[3]
+        dx, dw, _ = d.linear_backward(dy, x, w, z, kind, torch.float32, torch.float32)
+        _split_check(dx, dz, w64, "dx")
+        _split_check(dw, dz.T, x64, "dw")
+        again = d.linear_backward(dy, x, w, z, kind, torch.float32, torch.float32)
+        assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.parametrize("M,I,H", [(1, 1, 1), (3, 5, 9), (65, 130, 1000), (333, 343, 1000), (2000, 520, 136)])
+def test_float32_gradients_of_a_gated_product(d, M, I, H):
+    r = np.random.default_rng(M + I)
+    x, x64 = _mat(r, M, H)
+    w, w64 = _mat(r, 2 * I, H, 0.1)
+    h, h64 = _mat(r, M, 2 * I, 1.5)
+    da, da64 = _mat(r, M, I, 0.1)
+    for kind in ("silu", "none"):
+        banner(f"float32 gradients of gated {kind}, {M}x{I}x{H}")
+        dh = od.gated_linear_backward(da64, x64, w64, h64, kind)[2]
+        dx, dw = d.gated_linear_backward(da, x, w, h, kind, torch.float32, torch.float32)
+        _split_check(dx, dh, w64, "dx")
+        _split_check(dw, dh.T, x64, "dw13")
+        # one gradient of each type, and one alone
+        dx16, dw32 = d.gated_linear_backward(da, x, w, h, kind)
+        assert torch.equal(dw32, dw)
+        _grad_check(dx16, None, None, (dh @ w64, None, None, dh), None, x64, w64, True, "bf16", None, "dx bf16")
+        assert torch.equal(d.gated_linear_backward(da, x, w, h, kind, need_dx=False)[1], dw)
+
+
+def test_bf16_dz_on_request_and_infinite_dz(d):
+    banner("dz_dtype bf16; infinite dz")
+    M, N, K = 300, 264, 136
+    r = np.random.default_rng(6)
+    x, x64 = _mat(r, M, K)
+    w, w64 = _mat(r, N, K, 0.1)
+    dy, dy64 = _mat(r, M, N, 0.1)
+    z, z64 = _mat(r, M, N, 1.5)
+    f32, b16 = torch.float32, torch.bfloat16
+    got = d.linear_backward(dy, x, w, z, "silu", f32, f32, need_dbias=True, dz_dtype=b16)
+    _grad_check(*got, od.linear_backward(dy64, x64, w64, z64, "silu"), dy64, x64, w64, True, "f32", "f32", "bf16 dz")
+    full = d.linear_backward(dy, x, w, z, "silu", f32, f32, need_dbias=True)
+    assert not torch.equal(got[1], full[1]) and torch.equal(got[2], full[2])
+    # bf16 gradients and exact products are the same either way
+    for act, zz, dt in (("silu", z, b16), ("none", None, f32)):
+        a, b = (d.linear_backward(dy, x, w, zz, act, dt, dt, dz_dtype=t) for t in (None, b16))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    h, h64 = _mat(r, M, 2 * N, 1.5)
+    w13, w13_64 = _mat(r, 2 * N, K, 0.1)
+    gx, gw = d.gated_linear_backward(dy, x, w13, h, "gelu", f32, f32, dz_dtype=b16)
+    wx, ww, dh = od.gated_linear_backward(dy64, x64, w13_64, h64, "gelu")
+    _grad_check(gx, gw, None, (wx, ww, None, dh), None, x64, w13_64, True, "f32", "f32", "gated bf16 dz")
+    # an infinity in dz is one in the products, not the NaN of its rounding's rest
+    dy[5, 7] = float("inf")
+    z[5, 7] = 1.0
+    dx, dw, _ = d.linear_backward(dy, x, w, z, "silu", f32, f32)
+    assert torch.isinf(dx[5]).all() and torch.isinf(dw[7]).all()
+    rows, cols = [i for i in range(M) if i != 5], [i for i in range(N) if i != 7]
+    assert torch.isfinite(dx[rows]).all() and torch.isfinite(dw[cols]).all()
+    need = d.linear_backward_workspace_bytes(dy, x, w, "silu")
+    assert need > d.linear_backward_workspace_bytes(dy, x, w, "silu", b16)
+    with pytest.raises(TypeError):
+        d.linear_backward(dy, x, w, z, "silu", dz_dtype=torch.float16)
