@@ -18,8 +18,9 @@ def _f64(a):
     return None if a is None else np.asarray(a, np.float64)
 
 
-def _erf(z):
-    return np.array([math.erf(v) for v in np.ravel(z)], np.float64).reshape(np.shape(z))
+def _normal_cdf(z):
+    """By erfc, which keeps its digits where the value is near 0."""
+    return np.array([0.5 * math.erfc(-v / math.sqrt(2.0)) for v in np.ravel(z)], np.float64).reshape(np.shape(z))
 
 
 def act(kind, z):
@@ -29,7 +30,7 @@ def act(kind, z):
     if kind == "silu":
         return z / (1.0 + np.exp(-z))
     if kind == "gelu":
-        return 0.5 * z * (1.0 + _erf(z / math.sqrt(2.0)))
+        return z * _normal_cdf(z)
     if kind == "relu":
         return np.where(z > 0, z, 0.0)
     raise ValueError(kind)
@@ -43,7 +44,7 @@ def act_grad(kind, z):
         sig = 1.0 / (1.0 + np.exp(-z))
         return sig * (1.0 + z * (1.0 - sig))
     if kind == "gelu":
-        return 0.5 * (1.0 + _erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+        return _normal_cdf(z) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
     if kind == "relu":
         return (z > 0).astype(np.float64)
     raise ValueError(kind)

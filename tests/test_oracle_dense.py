@@ -33,6 +33,14 @@ def test_activations_at_known_points():
         assert np.allclose(od.act_grad(k, z), num, atol=1e-8), k
 
 
+def test_gelu_tail():
+    # Phi(-8), Phi(-12) from tables of the normal distribution
+    for z, phi in ((-8.0, 6.22096057427178e-16), (-12.0, 1.776482112077679e-33)):
+        pdf = math.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+        assert od.act("gelu", [z])[0] == pytest.approx(z * phi, rel=1e-12)
+        assert od.act_grad("gelu", [z])[0] == pytest.approx(phi + z * pdf, rel=1e-12)
+
+
 def test_layer_norm_by_hand():
     # deviations -1, 1 around 3: var 1, eps 3 -> rstd 1/2
     y, mean, rstd, s = od.layer_norm([[1.0, 3.0]], gamma=[2.0, 4.0], beta=[0.5, -0.5], eps=3.0, residual=[[1.0, 1.0]])
