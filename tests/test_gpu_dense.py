@@ -18,6 +18,8 @@ v = 2^-8 (bf16: 8 significant bits):
 * an output rounded to its type: u or v of the value.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -718,3 +720,67 @@ def test_bf16_dz_on_request_and_infinite_dz(d):
     assert need > d.linear_backward_workspace_bytes(dy, x, w, "silu", b16)
     with pytest.raises(TypeError):
         d.linear_backward(dy, x, w, z, "silu", dz_dtype=torch.float16)
+
+
+# ---------------------------------------------------------------------------
+# activations at exact arguments
+# ---------------------------------------------------------------------------
+
+# z of either sign from the smallest normal float to past where e^z and the
+# normal distribution's tail leave float32's range
+_Z = np.sort(np.concatenate([s * np.concatenate([np.linspace(0.0, 16.0, 3001), np.linspace(16.0, 120.0, 1000),
+                                                 2.0 ** np.linspace(-126, 0, 300)]) for s in (1.0, -1.0)]).astype(np.float32))
+
+
+def _act_terms(kind, z):
+    """(act, |terms of act'| summed, act') in float64, no difference of near values."""
+    if kind == "relu":
+        return np.maximum(z, 0.0), (z > 0) * 1.0, (z > 0) * 1.0
+    if kind == "silu":
+        p, q = 1.0 / (1.0 + np.exp(-z)), 1.0 / (1.0 + np.exp(z))
+        return z * p, p * (1.0 + np.abs(z) * q), p * (1.0 + z * q)
+    phi = 0.5 * np.array([math.erfc(-v / math.sqrt(2.0)) for v in z])
+    pdf = np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    return z * phi, phi + np.abs(z) * pdf, phi + z * pdf
+
+
+@pytest.mark.parametrize("tokens", [1, 80])
+@pytest.mark.parametrize("kind", ["gelu", "relu"])
+def test_activation_at_exact_arguments(d, kind, tokens):
+    """act and act' within 2^-20 of their value (of the sum of act's two terms'
+    sizes, which cancel at its zero), where float32 has one: z = bias exactly,
+    as x = 0, and the bias gradient of one row of ones is act'(z)."""
+    banner(f"activation {kind} {tokens}")
+    z64 = _Z.astype(np.float64)
+    n = z64.size
+    z = torch.from_numpy(_Z).cuda()
+    e = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    tiny = 2.0 ** -126
+    f, terms, df = _act_terms(kind, z64)
+    y, saved = d.linear(e(tokens, 8), e(n, 8), z, kind, out_dtype=torch.float32, save_z=True)
+    assert torch.equal(saved, z.expand(tokens, n))
+    _close(y, np.broadcast_to(f, (tokens, n)), 2.0 ** -20 * np.abs(f) + tiny, "f32", f"{kind}")
+    _, _, db = d.linear_backward(e(1, n) + 1, e(1, 8), e(n, 8), z[None], kind, need_dx=False, need_dw=False,
+                                 need_dbias=True)
+    _close(db, df, 2.0 ** -20 * terms + tiny, "f32", f"{kind}'")
+    # the gate of the gated product: g exact (one product with 1), u = 1
+    g = z.bfloat16()
+    g64 = host(g).astype(np.float64)
+    f, terms, df = _act_terms(kind, g64)
+    one = e(tokens, 1) + 1
+    w13 = torch.cat([g[:, None], torch.ones_like(g)[:, None]])
+    a, h = d.gated_linear(one, w13, kind, torch.float32, save_h=True)
+    assert torch.equal(h[0], w13[:, 0])
+    _close(a, np.broadcast_to(f, (tokens, n)), 2.0 ** -20 * np.abs(f) + tiny, "f32", f"gated {kind}")
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "relu"])
+def test_activation_of_infinities_and_nan(d, kind):
+    """As in the formulas: z / (1 + e^-z) and z (1 + erf) / 2 at minus infinity
+    are infinity times 0, max(z, 0) is 0."""
+    banner(f"activation {kind}, infinities")
+    z = torch.tensor([float("inf"), -float("inf"), float("nan"), 3.0], device="cuda")
+    x, w = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((1, 8), (4, 8)))
+    y = host(d.linear(x, w, z, kind, out_dtype=torch.float32)[0])[0]
+    assert y[0] == np.inf and np.isnan(y[2]) and np.isfinite(y[3])
+    assert y[1] == 0 if kind == "relu" else np.isnan(y[1])
