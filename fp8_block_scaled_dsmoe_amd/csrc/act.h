@@ -8,9 +8,15 @@
 
 namespace dsmoe {
 
-// 1 / (1 + e^-z): e^-z overflows to infinity for z < -88, where the
-// reciprocal gives the correct 0
-__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+// 1 / (1 + e^-z) in p and 1 / (1 + e^z) in q.  Both come from e^-|z|, which
+// does not overflow, so p keeps its digits where it is small: a reciprocal of
+// 1 + e^-z would be 0 from z = -87.4 on, where float32 still has z p.  The
+// reciprocal is the approximate one, within an ulp, of a value in [1, 2].
+__device__ __forceinline__ void sigmoid_f32(float z, float& p, float& q) {
+  const float t = expf(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + t);
+  p = z < 0.0f ? t * r : r;
+  q = z < 0.0f ? r : t * r;
+}
 
 // P(-t) and e = exp(-t^2 / 2) for t = min(|z|, 16), P the normal distribution
 // (at 16 both are 0 in float32).  P(-t) = e g(t), where g is smooth and falls
@@ -41,7 +47,11 @@ __device__ __forceinline__ float normal_tail_f32(float z, float& e) {
 // ReLU keeps NaN, as z * (z > 0) does
 __device__ __forceinline__ float act_f32(int act, float z) {
   switch (act) {
-    case DSMOE_ACT_SILU: return z * sigmoid_f32(z);
+    case DSMOE_ACT_SILU: {
+      float p, q;
+      sigmoid_f32(z, p, q);
+      return z * p;
+    }
     case DSMOE_ACT_GELU: {
       float e;
       const float p = normal_tail_f32(z, e);
@@ -56,9 +66,10 @@ __device__ __forceinline__ float act_f32(int act, float z) {
 __device__ __forceinline__ void act_and_grad_f32(int act, float z, float& f, float& d) {
   switch (act) {
     case DSMOE_ACT_SILU: {
-      const float p = sigmoid_f32(z);
+      float p, q;
+      sigmoid_f32(z, p, q);
       f = z * p;
-      d = p * (1.0f + z * (1.0f - p));
+      d = p * (1.0f + z * q);
       break;
     }
     case DSMOE_ACT_GELU: {

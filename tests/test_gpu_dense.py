@@ -745,7 +745,7 @@ def _act_terms(kind, z):
 
 
 @pytest.mark.parametrize("tokens", [1, 80])
-@pytest.mark.parametrize("kind", ["gelu", "relu"])
+@pytest.mark.parametrize("kind", ["silu", "gelu", "relu"])
 def test_activation_at_exact_arguments(d, kind, tokens):
     """act and act' within 2^-20 of their value (of the sum of act's two terms'
     sizes, which cancel at its zero), where float32 has one: z = bias exactly,
