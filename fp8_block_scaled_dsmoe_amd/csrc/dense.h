@@ -89,6 +89,13 @@ struct DenseGemm {
   void* workspace;        // dense_gemm_workspace_bytes() bytes
 };
 size_t dense_gemm_workspace_bytes(const DenseGemm& p);
+// The kernels that a product of at most 2^28 rows takes: few tokens (1) or
+// tiles (0), then of its one or two launches of tiles the shape (the index in
+// kShapes) and splits of K, and the first column of the second (0: none).
+struct DenseKernels {
+  int64_t few_tokens, shape, splits, cut, rest_shape, rest_splits;
+};
+DenseKernels dense_gemm_kernels(const DenseGemm& p);
 hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s);
 
 // dense_skinny.hip: the same products for p.M <= 64 and both operands by rows;

@@ -142,6 +142,24 @@ bool f32_gradient(const void* dx, int dxt, const void* dw, int dwt) {
 
 extern "C" {
 
+// Not part of the interface: lets tests hold the sizes they use to the kernels
+// they are for.  The kernels of one product of 16-byte rows: 0 y of
+// dsmoe_linear, 1 its dx, 2 its dw (M, N, K as there), 3 dsmoe_gated_linear (N
+// its I, K its H); the gated backward's are those of 1 and 2 with N = 2 I.
+int dsmoe_dense_kernels(int product, int64_t M, int64_t N, int64_t K, int64_t out[6]) {
+  if (product < 0 || product > 3 || M < 1 || M > (1 << 28) || !half_dim_ok(N) || !dim_ok(K)) return DSMOE_ERR_SHAPE;
+  const int64_t ldn = round_up(N, 8), ldk = round_up(K, 8);
+  DenseGemm g = product == 0   ? forward_product(nullptr, ldk, nullptr, ldk, M, N, K, DenseEpi::kLinear)
+                : product == 1 ? dx_product(nullptr, ldn, true, nullptr, ldk, M, N, K)
+                : product == 2 ? dw_product(nullptr, ldn, true, nullptr, ldk, M, N, K)
+                               : forward_product(nullptr, ldk, nullptr, ldk, M, N, K, DenseEpi::kGated);
+  g.a.padded = g.b.padded = true;
+  const dsmoe::DenseKernels k = dsmoe::dense_gemm_kernels(g);
+  const int64_t v[6] = {k.few_tokens, k.shape, k.splits, k.cut, k.rest_shape, k.rest_splits};
+  for (int i = 0; i < 6; ++i) out[i] = v[i];
+  return DSMOE_OK;
+}
+
 dsmoe_status dsmoe_layer_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int xt,
                               const void* gamma, const void* beta, int pt, int64_t rows, int64_t cols,
                               float eps, void* y, int64_t ldy, void* sum, int64_t lds, float* mean,

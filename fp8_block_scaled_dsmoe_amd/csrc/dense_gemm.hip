@@ -1046,6 +1046,12 @@ size_t dense_gemm_workspace_bytes(const DenseGemm& p) {
   return most;
 }
 
+DenseKernels dense_gemm_kernels(const DenseGemm& p) {
+  const Plan pl = make_plan(p);
+  return DenseKernels{few_tokens(p, pl),  static_cast<int>(pl.first.shape), pl.first.splits, pl.cut,
+                      pl.cut ? static_cast<int>(pl.rest.shape) : 0, pl.cut ? pl.rest.splits : 0};
+}
+
 hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t s) {
   return by_row_ranges(p, [&](const DenseGemm& q) { return launch_range(q, s); });
 }

@@ -213,3 +213,24 @@ def test_header_is_c99_and_links_from_c(tmp_path, d):
     assert r.returncode == 0, r.stderr
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout.strip() == "ok", (out.returncode, out.stderr)
+
+
+def test_sizes_that_run_every_dense_kernel(d):
+    """Each size of dense_kernels.SIZES takes the kernels that its GPU test is
+    there for, and together they are every tile shape in every form."""
+    import dense_kernels as dk
+    for size, want in dk.SIZES.items():
+        assert dk.kernels(d.lib, *size) == want, size
+    for product in dk.PRODUCTS:
+        rows = [v for k, v in dk.SIZES.items() if k[0] == product]
+        assert {s for s, split, rest in rows if not split and not rest} == set(dk.SHAPES), product
+        assert {rest for _, _, rest in rows if rest} == set(dk.SHAPES) - {"256x256"}, product
+        assert any(split for _, split, _ in rows), product
+    # what gated backward runs on a training batch: both products cut in two
+    for product in ("dx", "dw"):
+        assert dk.kernels(d.lib, product, 4096, 2 * 2048, 7168) == ("256x256", False, "256x192")
+    assert dk.kernels(d.lib, "y", 4, 32, 64)[0] == dk.kernels(d.lib, "gated", 64, 64, 64)[0] == "few tokens"
+    f = d.lib.dsmoe_dense_kernels
+    out = (ctypes.c_int64 * 6)()
+    for bad in ((4, 8, 8, 8), (-1, 8, 8, 8), (0, 0, 8, 8), (0, 8, 0, 8), (0, 8, 8, 0), (0, (1 << 28) + 1, 8, 8)):
+        assert f(*bad, ctypes.byref(out)) == SHAPE

@@ -667,7 +667,8 @@ def test_float32_gradients_of_an_activation(d, M, N, K):
         assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
-@pytest.mark.parametrize("M,I,H", [(1, 1, 1), (3, 5, 9), (65, 130, 1000), (333, 343, 1000), (2000, 520, 136)])
+@pytest.mark.parametrize("M,I,H", [(1, 1, 1), (3, 5, 9), (65, 130, 1000), (333, 343, 1000), (2000, 520, 136),
+                                   (538, 2316, 5156)])   # dw in two launches
 def test_float32_gradients_of_a_gated_product(d, M, I, H):
     r = np.random.default_rng(M + I)
     x, x64 = _mat(r, M, H)
