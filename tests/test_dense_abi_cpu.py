@@ -162,6 +162,24 @@ def test_gated_linear_backward_refusals(d):
     assert _gated_bwd(d, M=0, dw=None) == OK
 
 
+def test_forward_workspace_refusals(d):
+    """Sizes that split K or copy an operand, so that a workspace is needed."""
+    ws = ctypes.c_void_p(1 << 21)
+    for call, query, size in (
+            (_linear, d.lib.dsmoe_linear_workspace_bytes, dict(M=769, N=264, K=3856)),
+            (_gated, d.lib.dsmoe_gated_linear_workspace_bytes, dict(M=328, H=3880, I=328))):
+        M, a, b = size.values()
+        K, N = (b, a) if "K" in size else (a, b)
+        wide = dict(ldx=K, ldw=K, **({"ldy": N} if "K" in size else {"lda": N}), **size)
+        aligned, packed = query(A, K, A, K, *size.values()), query(ctypes.c_void_p((1 << 20) + 2), K, A, K, *size.values())
+        assert aligned > 0 and packed >= aligned + M * K * 2
+        for need, x in ((aligned, A), (packed, ctypes.c_void_p((1 << 20) + 2))):
+            assert call(d, **wide, x=x, ws=ws, wsn=need - 1) == WORKSPACE
+            assert call(d, **wide, x=x, ws=None, wsn=need) == WORKSPACE
+            assert call(d, **wide, x=x) == WORKSPACE
+            assert call(d, **wide, x=x, ws=ctypes.c_void_p((1 << 21) + 128), wsn=need) == ALIGN
+
+
 def test_backward_calls_take_the_bf16_dz_flag_and_no_other(d):
     flag = 16
     args = (A, 32, A, 64, A, 64)
