@@ -16,10 +16,11 @@
 //                        the other reads
 //   dense_paired_kernel  128 x 256: the same with whole chunks
 //   dense_ring_kernel    smaller tiles: reads between a wave's own products
-// The matrix cores bound the large products: 8192^3 takes 0.73 to 0.75 ms, 1.47
-// to 1.50 PFLOP/s, the matrix cores busy 81 to 87% of the cycles, and the card
-// lowers its clock under this load (to 1.8 GHz of 2.4), so LDS and memory
-// traffic cost time through power as well.  For 256 x 256, four phases per
+// The matrix cores bound the large products: 8192^3 takes 0.74 to 0.76 ms, 1.45
+// to 1.49 PFLOP/s, the matrix cores busy 76% of the launch's cycles (80% of
+// those with a block on the CU), and the card lowers its clock under this load
+// (to 1.7 GHz of 2.4), so LDS and memory traffic cost time through power as
+// well.  For 256 x 256, four phases per
 // chunk (A0 B0, A0 B1, A1 B1, A1 B0) took 10% longer, with twice the barriers
 // and reads crowded into two of the phases; four waves of 128 x 128 with the
 // reads between their own products 9%.
@@ -490,7 +491,7 @@ struct Tile {
 // tile's products.  Once every wave has read a half into registers, its place
 // takes the same half of the chunk two ahead; the copies have a whole chunk to
 // arrive, and only two chunks are ever in LDS.  Waves w and w + 4 share a SIMD.
-// 4096^3 takes 95 to 99 us, by W's columns 97 to 100, both by columns 104 to 107.
+// 4096^3 takes 100 us, by W's columns 102, both by columns 106.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
@@ -783,7 +784,8 @@ __global__ __launch_bounds__(256) void zero_matrix_kernel(void* dst, int64_t ldd
 //   128 x 128  four stages, one per CU: when there is at most one tile per CU
 //              (1024 x 4096 x 4096 in 38 us; with two stages 45, 256 x 256 80)
 //   128 x 128  two stages, two per CU: a few tiles per CU and few chunks
-//              (16384 x 512 x 512 in 15.9 us; four stages 19.5, 256 x 256 22.7)
+//              (16384 x 512 x 256 in 11.5 us, 128 x 256 11.9; from 6 chunks on
+//              the two are within 3%: 16384 x 512 x 512 15.9 and 16.2)
 //   256 x 192  phased: what is left over when 256 x 256 tiles fill the card a
 //              whole number of times (see make_plan), and sizes it fits better
 //   128 x 256  three stages, one per CU: when 256 x 256 leaves CUs without a

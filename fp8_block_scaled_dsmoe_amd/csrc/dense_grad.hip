@@ -6,7 +6,7 @@
 // operand, 16 significant bits in all.
 // HBM bounds them: dy and z (or da and h) in, dz (dh) out.  Column sums alone of
 // 4096 x 7168 (58 MB): 13 us; the gated gradient of 4096 x 2 x 2048 (84 MB in
-// all): 21 us.
+// all): 20 us, 23 with the second operand (117 MB).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
