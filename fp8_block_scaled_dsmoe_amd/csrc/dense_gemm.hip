@@ -1,21 +1,7 @@
 // Matrix products of the dense feed-forward operators in bf16 with float32
-// sums: c[m][n] = sum_k a(m, k) b(n, k) and a fused epilogue.  Either operand
-// may be stored with the contraction index along its rows ("row" operands:
-// x and W forward, dz in dx) or across them ("k-row" operands: W in dx, dz
-// and x in dW).
-//
-// A block computes a BM x BN tile in steps of 64 of K ("chunks") with
-// v_mfma_f32_16x16x32_bf16.  Both operand tiles are split in two halves (rows
-// [0, BM/2) and [BM/2, BM), and so for B), and every wave owns an equal part of
-// each half.  Chunks come by asynchronous copies (buffer loads straight to
-// LDS, 16 bytes a lane) one to three chunks ahead; operands leave LDS as whole
-// fragments, k-row operands by the transposing read.  Three kernels differ in
-// how reads, copies and products meet:
-//   dense_phased_kernel  256 rows: a chunk in two phases (A0, A1), the two waves
-//                        of a SIMD half a phase apart, one multiplying while
-//                        the other reads
-//   dense_paired_kernel  128 x 256: the same with whole chunks
-//   dense_ring_kernel    smaller tiles: reads between a wave's own products
+// sums: c[m][n] = sum_k a(m, k) b(n, k) and a fused epilogue, in the tiles and
+// loops of tile.h.  Row operands are x and W forward and dz in dx; k-row operands
+// W in dx, dz and x in dW.
 // The matrix cores bound the large products: 8192^3 takes 0.74 to 0.76 ms, 1.45
 // to 1.49 PFLOP/s, the matrix cores busy 76% of the launch's cycles (80% of
 // those with a block on the CU), and the card lowers its clock under this load
@@ -30,24 +16,13 @@
 #include "act.h"
 #include "common.h"
 #include "dense.h"
+#include "tile.h"
 #include "vec8.h"
 
 namespace dsmoe {
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-#define DSMOE_LDS __attribute__((address_space(3)))
-template <typename T>
-__device__ __forceinline__ DSMOE_LDS T* lds_ptr(uint32_t at) {
-  return (DSMOE_LDS T*)static_cast<uintptr_t>(at);
-}
-
 constexpr int kChunk = 64;   // K per chunk
-constexpr int kXcds = 8;
 
 // ---------------------------------------------------------------------------
 // Epilogue: 8 adjacent columns of one row.
@@ -106,175 +81,6 @@ __device__ __forceinline__ void load_bias(const DenseGemm& p, int64_t n, float* 
   }
 }
 
-// ---------------------------------------------------------------------------
-// Operand halves: from memory to LDS, from LDS to MFMA operands.
-// ---------------------------------------------------------------------------
-
-// Asynchronous copy of 16 bytes per lane to lds + 16 lane (wave-uniform lds):
-// offset voff from the resource's base; past its range zeros are written.
-// Issued from assembly so that the compiler neither waits for it nor counts
-// it; the kernel waits for vmcnt itself.  A copy to LDS must not follow a
-// write of M0 directly (one wait state, which the compiler cannot add inside
-// assembly).
-__device__ __forceinline__ void copy16(const i32x4& rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
-               "s"(lds)
-               : "memory", "m0");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  static_assert(N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
-
-// One half (HR rows x 64 of K) of an operand tile in LDS, HR * 128 bytes.
-//
-// Row operand: row r is 128 bytes of 8 16-byte segments, segment s stored in
-// place s ^ (r % 8), so that the 16 rows an operand read touches at one
-// segment spread over all banks.
-// K-row operand: k is a row of HR * 2 bytes of HR / 16 32-byte blocks (16
-// columns), block b stored in place b ^ key(k); operands are read with the
-// transposing LDS read, which takes four rows of k x 16 columns per 16 lanes
-// and gives each lane its column: the key separates the rows that one read
-// touches.
-template <int HR, bool KROWS, int NW>
-struct Half {
-  static constexpr int kBytes = HR * 128;
-  static constexpr int kAll = HR / 8;                      // copies of 1 KB
-  static constexpr int kCopies = (kAll + NW - 1) / NW;     // of a wave
-  static constexpr int kSegs = HR / 8;                     // k-row operand: 16-byte segments of a row
-  // the wave's i-th copy; where they do not come out even the last one is
-  // made more than once (the same bytes to the same place)
-  static __device__ __forceinline__ int index(int wave, int i) { return min(wave * kCopies + i, kAll - 1); }
-
-  static __device__ __forceinline__ int key(int k) {
-    if constexpr (HR == 128) return (k & 3) | ((k >> 3) & 1) << 2;
-    if constexpr (HR == 64) return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
-    return (k >> 3) & 1;
-  }
-};
-
-// What a wave copies of one half, chunk by chunk: a buffer resource that starts
-// at the half's chunk and ends with its last valid element, and the lane's
-// offsets in it.  advance() is a few scalar instructions while whole chunks
-// are left; the offsets and the range change only from the last one on.
-// (Masking every copy by its k, and a range computed anew per chunk, cost the
-// multiplies of a one-wave-per-SIMD loop 8 to 10 cycles per vector
-// instruction.)
-template <int HR, bool KROWS, int NW>
-struct Source {
-  using H = Half<HR, KROWS, NW>;
-  uint64_t base;                  // byte address of the half's (row 0, chunk's first k)
-  int32_t range;                  // bytes from base that may be read
-  uint32_t ld2;                   // row stride in bytes
-  int32_t k_left;                 // valid k from base on
-  int32_t cols2;                  // k-row operand: bytes of a row's valid columns
-  int32_t lane_k;                 // row operand: first k of the lane's segment
-  uint32_t voff[H::kCopies];
-
-  __device__ __forceinline__ Source() {}
-  // rows [r0, r0 + HR) of the operand, chunks from k0 on, k_end: end of valid k
-  __device__ __forceinline__ Source(const Operand& o, int64_t r0, int64_t rows, int64_t k0, int64_t k_end, int wave,
-                                    int lane) {
-    ld2 = static_cast<uint32_t>(o.ld * 2);
-    const int64_t left = min(static_cast<int64_t>(HR), rows - r0);
-    k_left = left > 0 ? static_cast<int32_t>(k_end - k0) : 0;
-    lane_k = 8 * ((lane & 7) ^ (lane >> 3));
-    if constexpr (KROWS) {
-      base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(k0 * o.ld + r0) * 2;
-      cols2 = left > 0 ? static_cast<int32_t>(left) * 2 : 0;
-      range = (kChunk - 1) * static_cast<int32_t>(ld2) + cols2;
-    } else {
-      base = reinterpret_cast<uint64_t>(o.p) + static_cast<uint64_t>(r0 * o.ld + k0) * 2;
-      range = left > 0 ? static_cast<int32_t>(left - 1) * static_cast<int32_t>(ld2) + 2 * k_left : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < H::kCopies; ++i) {
-      const int j = H::index(wave, i);
-      if constexpr (KROWS) {
-        const int k = (j * 64 + lane) / H::kSegs, seg = (j * 64 + lane) % H::kSegs;
-        const int col = ((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8;
-        voff[i] = col < left ? static_cast<uint32_t>(k) * ld2 + col * 2 : kOutside;
-      } else {
-        voff[i] = static_cast<uint32_t>(8 * j + lane / 8) * ld2 + 2 * lane_k;
-      }
-    }
-    if (k_left < kChunk) cut();
-  }
-  // past every range (the largest is 128 rows of 2^23 bytes)
-  static constexpr uint32_t kOutside = 0x80000000u;
-  // The last chunk, and those past the end: what is past k_left reads as zero.
-  __device__ __forceinline__ void cut() {
-    asm volatile("");   // a branch around it, not selects in every chunk
-    if constexpr (KROWS) {
-      range = k_left > 0 ? (k_left - 1) * static_cast<int32_t>(ld2) + cols2 : 0;
-    } else {
-      if (k_left <= 0) range = 0;
-#pragma unroll
-      for (int i = 0; i < H::kCopies; ++i)
-        if (lane_k >= k_left) voff[i] = kOutside;   // it would read the next row
-    }
-  }
-  __device__ __forceinline__ void advance() {
-    if constexpr (KROWS) {
-      base += ld2 * kChunk;
-    } else {
-      base += 2 * kChunk;
-      range -= 2 * kChunk;   // may pass 0 only where cut() makes it 0
-    }
-    k_left -= kChunk;
-    if (k_left < kChunk) cut();
-  }
-  // Issue this wave's copies of the current chunk to the half at lds.
-  __device__ __forceinline__ void copy(uint32_t lds, int wave) const {
-    // wave-uniform: into scalar registers
-    i32x4 r;
-    r.x = __builtin_amdgcn_readfirstlane(static_cast<int>(base & 0xffffffffu));
-    r.y = __builtin_amdgcn_readfirstlane(static_cast<int>(base >> 32));   // below bit 48: stride 0, a raw buffer
-    r.z = __builtin_amdgcn_readfirstlane(range);
-    r.w = 0x00020000;
-#pragma unroll
-    for (int i = 0; i < H::kCopies; ++i)
-      copy16(r, voff[i],
-             __builtin_amdgcn_readfirstlane(lds + static_cast<uint32_t>(H::index(wave, i)) * 1024));
-  }
-};
-
-// A wave's reader of T 16-row operand fragments from row0 of a half:
-// fragment i, K step kk (of 2): lane l holds row l % 16, k = 32 kk + 8 (l / 16)
-// + [0, 8).
-template <int HR, bool KROWS, int T>
-struct Reader {
-  uint32_t at[KROWS ? T : 2];
-  __device__ __forceinline__ Reader(int row0, int lane) {
-    if constexpr (KROWS) {
-      const int s = lane & 15, g = lane >> 4;
-      const int k = 8 * g + (s >> 2);      // key() ignores the bits the reads below add to k
-#pragma unroll
-      for (int i = 0; i < T; ++i)
-        at[i] = k * HR * 2 + (((row0 / 16 + i) ^ Half<HR, true, 1>::key(k)) << 5) + (s & 3) * 8;
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-        at[kk] = (row0 + (lane & 15)) * 128 + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
-    }
-  }
-  // half: the half's place in the stage (a constant: it goes into the
-  // instruction's offset)
-  __device__ __forceinline__ bf16x8 read(uint32_t stage, uint32_t half, int i, int kk) const {
-    if constexpr (KROWS) {
-      DSMOE_LDS char* a = lds_ptr<char>(stage + at[i]) + (half + kk * (32 * HR * 2));
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSMOE_LDS s16x4*)a);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSMOE_LDS s16x4*)(a + 4 * HR * 2));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-      return *(DSMOE_LDS const bf16x8*)(lds_ptr<char>(stage + at[kk]) + (half + i * 2048));
-    }
-  }
-};
-
 // Blocks are dispatched round-robin over the 8 XCDs: give each XCD a run of
 // consecutive tiles, and number the tiles in bands of 4 row tiles, column by
 // column, so that the tiles an XCD works on at once (about 4 x 8) share their
@@ -290,48 +96,22 @@ __device__ __forceinline__ void tile_of_block(uint32_t b, uint32_t n, int32_t ti
   tn = static_cast<int32_t>(in / rows);
 }
 
-// What a block and its waves work on.  HM, HN: rows of a half of A and of B;
-// WM x WN waves.  kGated: half 0 of B holds gate rows, half 1 the same up
-// rows, so a lane has both sums of its columns.
+// What a block and its waves work on (TileCore), its part of the problem and its
+// epilogue.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
-struct Tile {
-  static constexpr bool kGated = EPI == DenseEpi::kGated;
-  static constexpr int NW = WM * WN;
-  static constexpr int TM = HM / WM / 16, TN = HN / WN / 16;   // fragments of a wave per half
-  using SA = Source<HM, AT, NW>;
-  using SB = Source<HN, BT, NW>;
-  static constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
-  static constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes;
-  // a stage of LDS and the places of the halves in it
-  static constexpr uint32_t kStage = 2 * (AB + BB), kA0 = 0, kA1 = AB, kB0 = 2 * AB, kB1 = 2 * AB + BB;
-  static constexpr int kOutStride = 2 * HN + 4;   // floats between rows of results in LDS
-  static constexpr int lds_bytes(int stages) {
-    const int a = stages * kStage, b = HM * kOutStride * 4;
-    return a > b ? a : b;
-  }
-  typedef f32x4 Acc[2][2][TM][TN];   // [half of A][half of B]
+struct Tile : TileCore<Elem::kBf16, HM, HN, WM, WN, AT, BT, EPI == DenseEpi::kGated, false> {
+  using Core = TileCore<Elem::kBf16, HM, HN, WM, WN, AT, BT, EPI == DenseEpi::kGated, false>;
+  using typename Core::Acc;
+  using typename Core::SA;
+  using typename Core::SB;
+  using Core::a0, Core::a1, Core::b0, Core::b1, Core::c0, Core::c1, Core::get, Core::kGated, Core::kRowsAtOnce,
+      Core::kRuns, Core::m0, Core::n0, Core::put;
 
   const TileArgs& t;
   const DenseGemm& p;
-  const int lane, wave, wm, wn;
-  int32_t split, c0, c1;   // split of K, its chunks
-  int64_t m0, n0;
-  SA a0, a1;
-  SB b0, b1;
-  const Reader<HM, AT, TM> ra;
-  const Reader<HN, BT, TN> rb;
-  const uint32_t lds;
+  int32_t split;   // of K
 
-  __device__ __forceinline__ Tile(const TileArgs& args, const uint8_t* mem)
-      : t(args),
-        p(args.p),
-        lane(threadIdx.x & 63),
-        wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-        wm(wave / WN),
-        wn(wave % WN),
-        ra(wm * (HM / WM), lane),
-        rb(wn * (HN / WN), lane),
-        lds(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(mem))) {
+  __device__ __forceinline__ Tile(const TileArgs& args, const uint8_t* mem) : Core(mem), t(args), p(args.p) {
     const uint32_t per_split = static_cast<uint32_t>(t.tiles_m) * t.tiles_n;
     split = blockIdx.x / per_split;
     int32_t tm, tn;
@@ -343,65 +123,12 @@ struct Tile {
     const int64_t k0 = static_cast<int64_t>(c0) * kChunk;
     const int64_t ka = min(t.a_k, static_cast<int64_t>(c1) * kChunk);
     const int64_t kb = min(t.b_k, static_cast<int64_t>(c1) * kChunk);
-    a0 = SA(p.a, m0, t.a_r, k0, ka, wave, lane);
-    a1 = SA(p.a, m0 + HM, t.a_r, k0, ka, wave, lane);
-    Operand up = p.b;   // kGated: the up rows are rows gate_n + n of b
-    if constexpr (kGated) up.p += p.gate_n * p.b.ld;
-    b0 = SB(p.b, n0, t.b_r, k0, kb, wave, lane);
-    b1 = SB(up, kGated ? n0 : n0 + HN, t.b_r, k0, kb, wave, lane);
-  }
-
-  // the wave's copies of the next chunk of a half into a stage
-  __device__ __forceinline__ void copy_a0(uint32_t stage) { a0.copy(stage + kA0, wave), a0.advance(); }
-  __device__ __forceinline__ void copy_a1(uint32_t stage) { a1.copy(stage + kA1, wave), a1.advance(); }
-  __device__ __forceinline__ void copy_b0(uint32_t stage) { b0.copy(stage + kB0, wave), b0.advance(); }
-  __device__ __forceinline__ void copy_b1(uint32_t stage) { b1.copy(stage + kB1, wave), b1.advance(); }
-
-  static __device__ __forceinline__ void clear(Acc& acc) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // The results pass through LDS, half of the tile's rows at a time, so that a
-  // thread finishes runs of 8 columns and a wave writes whole lines.
-  static constexpr int kRuns = (kGated ? HN : 2 * HN) / 8;   // of 8 columns
-  // rows that the block's threads take at once, a power of 2 (with 24 runs a
-  // quarter of the threads stay out)
-  static constexpr int rows_at_once(int per_row) {
-    int r = 1;
-    while (2 * r * per_row <= 64 * NW && 2 * r <= HM) r *= 2;
-    return r;
-  }
-  static constexpr int kRowsAtOnce = rows_at_once(kRuns);
-
-  // Half ha of the results to LDS.  A result lane holds row l % 16 of its A
-  // fragment and columns 4 (l / 16) + [0, 4) of its B fragment; rows 16 bytes
-  // off a multiple of 256 apart keep the writes of 16 rows on separate banks.
-  __device__ __forceinline__ void put(const f32x4 (&acc)[2][TM][TN]) const {
-    wait_lds();        // this wave's reads of LDS are done, and past the barrier
-    block_barrier();   // everyone's
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int r = wm * (HM / WM) + 16 * i + (lane & 15);
-          const int c = hb * HN + wn * (HN / WN) + 16 * j + 4 * (lane >> 4);
-          *lds_ptr<f32x4>(lds + (r * kOutStride + c) * 4) = acc[hb][i][j];
-        }
-    wait_lds();
-    block_barrier();
-  }
-  __device__ __forceinline__ void get(int r, int col, float* v) const {
-    const uint32_t at = lds + (r * kOutStride + col) * 4;
-    const f32x4 v0 = *lds_ptr<const f32x4>(at), v1 = *lds_ptr<const f32x4>(at + 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = v0[e], v[4 + e] = v1[e];
+    a0 = SA(p.a.p, p.a.ld, m0, t.a_r, k0, ka, this->wave, this->lane);
+    a1 = SA(p.a.p, p.a.ld, m0 + HM, t.a_r, k0, ka, this->wave, this->lane);
+    // kGated: the up rows are rows gate_n + n of b
+    const uint16_t* up = kGated ? p.b.p + p.gate_n * p.b.ld : p.b.p;
+    b0 = SB(p.b.p, p.b.ld, n0, t.b_r, k0, kb, this->wave, this->lane);
+    b1 = SB(up, p.b.ld, kGated ? n0 : n0 + HN, t.b_r, k0, kb, this->wave, this->lane);
   }
 
   // y = acc + bias + residual.  The residual of all of
@@ -486,216 +213,33 @@ struct Tile {
   }
 };
 
-// The 256-row tiles: two stages of LDS refilled half by half.  A chunk falls
-// into two phases, A0 with both halves of B and A1 with both, each half of the
-// tile's products.  Once every wave has read a half into registers, its place
-// takes the same half of the chunk two ahead; the copies have a whole chunk to
-// arrive, and only two chunks are ever in LDS.  Waves w and w + 4 share a SIMD.
-// 4096^3 takes 100 us, by W's columns 102, both by columns 106.
 template <int HM, int HN, int WM, int WN, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_phased_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
-  constexpr int TM = T::TM, TN = T::TN, LA = T::LA, LB = T::LB;
-  static_assert(T::NW == 8, "two waves per SIMD");
   __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(2)];
   T w(args, s_mem);
   typename T::Acc acc;
-  T::clear(acc);
-  bf16x8 fa[TM][2], fb[3][TN][2];
-
-  const uint32_t s0 = w.lds, s1 = w.lds + T::kStage;
-  w.copy_b0(s0);
-  w.copy_a0(s0);
-  w.copy_b1(s0);
-  w.copy_a1(s0);
-  w.copy_b0(s1);
-  w.copy_a0(s1);
-  w.copy_b1(s1);
-  wait_copies<2 * LA + 2 * LB>();   // this wave's part of B0, A0 and B1 of the first chunk
-  block_barrier();
-#define DSMOE_READ_A(stage, half)                                        \
-  _Pragma("unroll") for (int i = 0; i < TM; ++i)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fa[i][kk] = w.ra.read(stage, half, i, kk)
-#define DSMOE_READ_B(f, stage, half)                                     \
-  _Pragma("unroll") for (int j = 0; j < TN; ++j)                  \
-      _Pragma("unroll") for (int kk = 0; kk < 2; ++kk) fb[f][j][kk] = w.rb.read(stage, half, j, kk)
-  // The end of a phase's reads and copies: the reads are done (the halves may
-  // be refilled once all waves are past the barrier), and what the next phase
-  // reads is there (at most the copies of this phase and the last may still be
-  // on the way).  Then the phase's products: both halves of B with A's half
-  // ha, B0 in fb[0], B1 in fb[1].
-#define DSMOE_PHASE(ha)                                                                                          \
-  do {                                                                                                           \
-    wait_copies<2 * LA + 2 * LB>();                                                                              \
-    wait_lds();                                                                                                  \
-    block_barrier();                                                                                             \
-    __builtin_amdgcn_sched_barrier(0);                                                                           \
-    __builtin_amdgcn_s_setprio(1);                                                      \
-    _Pragma("unroll") for (int kk = 0; kk < 2; ++kk)                                                             \
-        _Pragma("unroll") for (int hb = 0; hb < 2; ++hb)                                                         \
-            _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                       \
-                _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[ha][hb][i][j] =                               \
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[hb][j][kk], fa[i][kk], acc[ha][hb][i][j], 0, 0, 0); \
-    __builtin_amdgcn_s_setprio(0);                                                      \
-    __builtin_amdgcn_sched_barrier(0);                                                                           \
-    block_barrier();                                                                    \
-  } while (0)
-  DSMOE_READ_B(0, s0, T::kB0);
-  wait_lds();
-  block_barrier();
-  if (w.wave >= 4) block_barrier();
-
-  // The next chunk's B0 is read in the second phase, to even out the phases'
-  // reads; it has registers of its own and moves at the end.
-  uint32_t st = s0, nx = s1;
-  for (int32_t c = w.c0; c < w.c1; ++c) {
-    DSMOE_READ_A(st, T::kA0);
-    DSMOE_READ_B(1, st, T::kB1);
-    __builtin_amdgcn_sched_barrier(0);
-    w.copy_a1(nx);
-    w.copy_b0(st);
-    DSMOE_PHASE(0);
-    DSMOE_READ_A(st, T::kA1);
-    DSMOE_READ_B(2, nx, T::kB0);
-    __builtin_amdgcn_sched_barrier(0);
-    w.copy_a0(st);
-    w.copy_b1(st);
-    DSMOE_PHASE(1);
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) fb[0][j][kk] = fb[2][j][kk];
-    const uint32_t sw = st;
-    st = nx;
-    nx = sw;
-  }
-  if (w.wave < 4) block_barrier();
-#undef DSMOE_READ_A
-#undef DSMOE_READ_B
-#undef DSMOE_PHASE
-  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
+  phased_loop(w, acc);
   w.finish(acc);
 }
 
-// 128 x 256: S stages of LDS, whole chunks.  The two waves of a SIMD run half a
-// chunk apart, one multiplying while the other reads all of its part of the
-// chunk; the stage that both have read takes the chunk S - 1 ahead.  Reads and
-// products of a chunk are about as long (16 reads, 32 products a wave), so
-// this beats reads between a wave's own products: 4096 x 2048 x 7168 in 92 us
-// instead of 103, by W's columns 97 instead of 122.  With 128 x 128, half the
-// products per barrier, it loses (2048^3 24.2 us instead of 22.9).
 template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_paired_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
-  constexpr int TM = T::TM, TN = T::TN, L = 2 * T::LA + 2 * T::LB;
-  static_assert(T::NW == 8, "two waves per SIMD");
   __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(S)];
   T w(args, s_mem);
   typename T::Acc acc;
-  T::clear(acc);
-  bf16x8 fa[2][TM][2], fb[2][TN][2];
-
-#define DSMOE_COPY(stage) w.copy_a0(stage), w.copy_b0(stage), w.copy_b1(stage), w.copy_a1(stage)
-  for (int i = 0; i < S - 1; ++i) DSMOE_COPY(w.lds + i * T::kStage);
-  wait_copies<(S - 2) * L>();
-  block_barrier();
-  if (w.wave >= 4) block_barrier();
-  uint32_t st = w.lds, free = w.lds + (S - 1) * T::kStage;
-  for (int32_t c = w.c0; c < w.c1; ++c) {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[h][i][kk] = w.ra.read(st, h ? T::kA1 : T::kA0, i, kk);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[h][j][kk] = w.rb.read(st, h ? T::kB1 : T::kB0, j, kk);
-      }
-    __builtin_amdgcn_sched_barrier(0);
-    // The last barrier was the other wave's end of reading the chunk before.
-    DSMOE_COPY(free);
-    wait_copies<(S - 2) * L>();   // this wave's part of the next chunk is there
-    wait_lds();
-    block_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[h >> 1][h & 1][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h & 1][j][kk], fa[h >> 1][i][kk],
-                                                                               acc[h >> 1][h & 1][i][j], 0, 0, 0);
-    __builtin_amdgcn_s_setprio(0);
-    __builtin_amdgcn_sched_barrier(0);
-    block_barrier();
-    free = st;
-    st = st + T::kStage == w.lds + S * T::kStage ? w.lds : st + T::kStage;
-  }
-#undef DSMOE_COPY
-  if (w.wave < 4) block_barrier();
-  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
+  paired_loop<S>(w, acc);
   w.finish(acc);
 }
 
-// Smaller tiles: S stages of LDS, latency and the copies' way bound them (2048^3
-// 21.5 to 24 us, 1000^3 8.6).  A chunk's fragments are read in two steps of
-// 32 of K, each while the products of the step before run; once a chunk's
-// second step is in registers in every wave, its stage is refilled with the
-// chunk S ahead.
 template <int HM, int HN, int WM, int WN, int S, bool AT, bool BT, DenseEpi EPI>
 __global__ __launch_bounds__(64 * WM * WN) void dense_ring_kernel(TileArgs args) {
   using T = Tile<HM, HN, WM, WN, AT, BT, EPI>;
-  constexpr int TM = T::TM, TN = T::TN, L = 2 * T::LA + 2 * T::LB;
   __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(S)];
   T w(args, s_mem);
   typename T::Acc acc;
-  T::clear(acc);
-  bf16x8 fa[2][2][TM], fb[2][2][TN];   // [step][half]
-
-#define DSMOE_COPY(stage) w.copy_a0(stage), w.copy_b0(stage), w.copy_b1(stage), w.copy_a1(stage)
-#define DSMOE_READ(kk, stage)                                                                              \
-  do {                                                                                                     \
-    _Pragma("unroll") for (int h = 0; h < 2; ++h) {                                                        \
-      _Pragma("unroll") for (int i = 0; i < TM; ++i) fa[kk][h][i] =                                        \
-          w.ra.read(stage, h ? T::kA1 : T::kA0, i, kk);                                               \
-      _Pragma("unroll") for (int j = 0; j < TN; ++j) fb[kk][h][j] =                                        \
-          w.rb.read(stage, h ? T::kB1 : T::kB0, j, kk);                                               \
-    }                                                                                                      \
-  } while (0)
-#define DSMOE_PRODUCTS(kk)                                                                                 \
-  _Pragma("unroll") for (int h = 0; h < 4; ++h)                                                            \
-      _Pragma("unroll") for (int i = 0; i < TM; ++i)                                                       \
-          _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[h >> 1][h & 1][i][j] =                        \
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][h & 1][j], fa[kk][h >> 1][i],                 \
-                                                      acc[h >> 1][h & 1][i][j], 0, 0, 0)
-  for (int i = 0; i < S; ++i) DSMOE_COPY(w.lds + i * T::kStage);
-  wait_copies<(S - 1) * L>();
-  block_barrier();
-  uint32_t st = w.lds;
-  DSMOE_READ(0, st);
-  for (int32_t c = w.c0; c < w.c1; ++c) {
-    const uint32_t nx = st + T::kStage == w.lds + S * T::kStage ? w.lds : st + T::kStage;
-    DSMOE_READ(1, st);
-    DSMOE_PRODUCTS(0);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_copies<(S - 2) * L>();   // the next chunk's copies of this wave
-    wait_lds();
-    block_barrier();
-    DSMOE_COPY(st);
-    DSMOE_READ(0, nx);
-    DSMOE_PRODUCTS(1);
-    __builtin_amdgcn_sched_barrier(0);
-    st = nx;
-  }
-#undef DSMOE_COPY
-#undef DSMOE_READ
-#undef DSMOE_PRODUCTS
-  wait_copies<0>();   // copies past the last chunk (zeros) land before LDS is used again
-  wait_lds();
+  ring_loop<S>(w, acc);
   w.finish(acc);
 }
 
