@@ -807,3 +807,12 @@ __all__ += ["ACTIVATIONS", "layer_norm", "layer_norm_backward", "layer_norm_back
             "linear_backward", "linear_workspace_bytes", "linear_backward_workspace_bytes", "gated_linear",
             "gated_linear_backward", "gated_linear_workspace_bytes", "gated_linear_backward_workspace_bytes",
             "dense_ffn_forward", "dense_ffn_backward"]
+
+# The routed experts' products outside FP8 build on both.
+from .experts import (EXPORTED_EXPERTS, grouped_gated_linear, grouped_gated_linear_backward,  # noqa: E402
+                      grouped_linear, grouped_linear_backward, int8_gated_linear, int8_linear, moe_ffn_backward,
+                      moe_ffn_forward, moe_ffn_int8_forward, quant_rows_int8, router_backward)
+
+__all__ += ["grouped_linear", "grouped_linear_backward", "grouped_gated_linear", "grouped_gated_linear_backward",
+            "router_backward", "quant_rows_int8", "int8_linear", "int8_gated_linear", "moe_ffn_forward",
+            "moe_ffn_backward", "moe_ffn_int8_forward"]

@@ -32,6 +32,7 @@ route  -- sigmoid affinity, bias-adjusted group-limited top-K, gates, permute
 layer  -- expert SwiGLU FFN and the whole MoE layer forward
 bias   -- auxiliary-loss-free bias update
 dense  -- dense feed-forward operators: layer norm, linear, gated linear (definitions)
+experts -- the routed experts' products outside FP8: by groups, in bf16 and 8-bit integers
 """
 
 from . import e4m3, quant, gemm, route, layer, bias  # noqa: F401
