@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsmoe.so")
 SOURCES = ["abi.hip", "quant.hip", "granularity.hip", "serving.hip", "route.hip", "gemm.hip", "backward.hip",
            "norm.hip", "dense_grad.hip", "dense_gemm.hip", "dense_skinny.hip", "dense_abi.hip", "grouped_gemm.hip",
-           "grouped_grad.hip", "int8_quant.hip", "experts_abi.hip"]
+           "grouped_int8.hip", "grouped_grad.hip", "int8_quant.hip", "experts_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

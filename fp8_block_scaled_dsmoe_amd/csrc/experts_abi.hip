@@ -31,6 +31,11 @@ bool source_ok(int64_t n, const int32_t* rows, int64_t R) { return rows_ok(n) &&
 // a row stride, looked at only where its matrix is given
 bool ld_ok(const void* p, int64_t ld, int64_t cols) { return !p || (ld >= cols && ld <= DSMOE_DENSE_MAX_DIM); }
 bool el_aligned(const void* p, int t) { return !p || aligned(p, esize(t)); }
+// no more elements than a card can hold, which keeps the numbers of tiles in 32 bits
+bool fits(int64_t G, int64_t R, int64_t N, int64_t K) {
+  constexpr int64_t kMost = int64_t{1} << 40;
+  return G * N <= kMost / K && (R == 0 || (N <= kMost / R && K <= kMost / R));
+}
 bool act_ok(int act) { return act >= DSMOE_ACT_NONE && act <= DSMOE_ACT_RELU; }
 bool grad_act_ok(int act) { return act_ok(act & ~DSMOE_DZ_BF16); }
 
@@ -121,7 +126,7 @@ dsmoe_status linear_call(bool i8, const void* x, int64_t ldx, const float* x_sca
                          int yt, void* z, int64_t ldz, void* workspace, size_t ws_bytes, void* stream) {
   if (!valid_dtype(yt)) return DSMOE_ERR_DTYPE;
   if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !(gated ? half_dim_ok(N) : dim_ok(N)) || !dim_ok(K) ||
-      !act_ok(act) || (i8 && K >= DSMOE_INT8_MAX_K) || (!offsets && G != 1))
+      !act_ok(act) || (i8 && K >= DSMOE_INT8_MAX_K) || (!offsets && G != 1) || !fits(G, R, gated ? 2 * N : N, K))
     return DSMOE_ERR_SHAPE;
   if (!ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(y, ldy, N) || !ld_ok(z, ldz, 2 * N)) return DSMOE_ERR_SHAPE;
   if (R == 0) return DSMOE_OK;
@@ -147,7 +152,8 @@ dsmoe_status linear_call(bool i8, const void* x, int64_t ldx, const float* x_sca
 
 size_t linear_bytes(bool i8, bool gated, const void* x, int64_t ldx, int64_t n, const int32_t* rows, const void* w,
                     int64_t ldw, int32_t G, int64_t R, int64_t N, int64_t K) {
-  if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !(gated ? half_dim_ok(N) : dim_ok(N)) || !dim_ok(K))
+  if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !(gated ? half_dim_ok(N) : dim_ok(N)) || !dim_ok(K) ||
+      !fits(G, R, gated ? 2 * N : N, K))
     return 0;
   return dsmoe::grouped_gemm_workspace_bytes(row_product(gated ? GroupedKind::kGated : GroupedKind::kLinear, i8,
                                                          rows_of(x, ldx, n, rows), w, ldw, Groups{nullptr, G, R}, N, K));
@@ -156,6 +162,28 @@ size_t linear_bytes(bool i8, bool gated, const void* x, int64_t ldx, int64_t n, 
 }  // namespace
 
 extern "C" {
+
+// Not part of the interface: lets tests hold the sizes they use to the kernels
+// they are for.  The tile shape (0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 32 x 128)
+// of R aligned rows in G groups: product 0 y of dsmoe_grouped_linear, 1 its dx, 2
+// its dw (N, K as there), 3 dsmoe_grouped_gated_linear (N its I, K its H), 4 and 5
+// the 8-bit forms of 0 and 3.
+int dsmoe_grouped_shape(int product, int32_t G, int64_t R, int64_t N, int64_t K) {
+  if (product < 0 || product > 5 || !groups_ok(G) || R < 1 || !rows_ok(R) || !half_dim_ok(N) || !dim_ok(K) ||
+      !fits(G, R, 2 * N, K))
+    return -1;
+  const RowsOf a = rows_of(nullptr, round_up(product == 1 || product == 2 ? N : K, 16), R, nullptr, true);
+  const RowsOf b = rows_of(nullptr, round_up(K, 16), R, nullptr, true);
+  const Groups g{nullptr, G, R};
+  const int64_t ld = round_up(K, 16);
+  switch (product) {
+    case 1: return dsmoe::grouped_gemm_shape(row_product(GroupedKind::kDx, false, a, nullptr, ld, g, K, N));
+    case 2: return dsmoe::grouped_gemm_shape(dw_product(a, b, g, N, K));
+    case 0:
+    case 4: return dsmoe::grouped_gemm_shape(row_product(GroupedKind::kLinear, product == 4, a, nullptr, ld, g, N, K));
+    default: return dsmoe::grouped_gemm_shape(row_product(GroupedKind::kGated, product == 5, a, nullptr, ld, g, N, K));
+  }
+}
 
 size_t dsmoe_grouped_linear_workspace_bytes(const void* x, int64_t ldx, int64_t n, const int32_t* rows,
                                             const void* w, int64_t ldw, int32_t G, int64_t R, int64_t N, int64_t K) {
@@ -173,7 +201,7 @@ size_t dsmoe_grouped_linear_backward_workspace_bytes(const void* dy, int64_t ldd
                                                      const int32_t* rows, const void* w, int64_t ldw, int32_t G,
                                                      int64_t R, int64_t N, int64_t K) {
   if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !source_ok(n_dy, dy_rows, R) || !dim_ok(N) ||
-      !dim_ok(K) || R == 0)
+      !dim_ok(K) || !fits(G, R, N, K) || R == 0)
     return 0;
   return gradients_bytes(rows_of(dy, lddy, n_dy, dy_rows), rows_of(x, ldx, n, rows), w, ldw, Groups{nullptr, G, R}, N,
                          K);
@@ -185,7 +213,7 @@ dsmoe_status dsmoe_grouped_linear_backward(const void* dy, int64_t lddy, int64_t
                                            int dwt, void* workspace, size_t ws_bytes, void* stream) {
   if (!valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
   if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !source_ok(n_dy, dy_rows, R) || !dim_ok(N) ||
-      !dim_ok(K) || (!offsets && G != 1))
+      !dim_ok(K) || (!offsets && G != 1) || !fits(G, R, N, K))
     return DSMOE_ERR_SHAPE;
   if (!ld_ok(dy, lddy, N) || !ld_ok(x, ldx, K) || !ld_ok(w, ldw, K) || !ld_ok(dx, lddx, K) || !ld_ok(dw, lddw, K))
     return DSMOE_ERR_SHAPE;
@@ -223,7 +251,8 @@ dsmoe_status dsmoe_grouped_gated_linear(const void* x, int64_t ldx, int64_t n, c
 size_t dsmoe_grouped_gated_linear_backward_workspace_bytes(const void* x, int64_t ldx, int64_t n,
                                                            const int32_t* rows, const void* w13, int64_t ldw,
                                                            int32_t G, int64_t R, int64_t H, int64_t I) {
-  if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !dim_ok(H) || !half_dim_ok(I)) return 0;
+  if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !dim_ok(H) || !half_dim_ok(I) || !fits(G, R, 2 * I, H))
+    return 0;
   return gated_layout(x, ldx, n, rows, w13, ldw, G, R, H, I).total;
 }
 dsmoe_status dsmoe_grouped_gated_linear_backward(const void* da, int64_t ldda, const void* x, int64_t ldx, int64_t n,
@@ -234,7 +263,7 @@ dsmoe_status dsmoe_grouped_gated_linear_backward(const void* da, int64_t ldda, c
                                                  void* workspace, size_t ws_bytes, void* stream) {
   if (!valid_dtype(dxt) || !valid_dtype(dwt)) return DSMOE_ERR_DTYPE;
   if (!groups_ok(G) || !rows_ok(R) || !source_ok(n, rows, R) || !dim_ok(H) || !half_dim_ok(I) || !grad_act_ok(act) ||
-      (!offsets && G != 1))
+      (!offsets && G != 1) || !fits(G, R, 2 * I, H))
     return DSMOE_ERR_SHAPE;
   const bool two = !(act & DSMOE_DZ_BF16);
   act &= ~DSMOE_DZ_BF16;

@@ -55,6 +55,8 @@ struct GroupedGemm {
 };
 size_t grouped_gemm_workspace_bytes(const GroupedGemm& p);
 hipError_t launch_grouped_gemm(const GroupedGemm& p, hipStream_t s);
+// The tile shape that a product takes (the index in kShapes).
+int grouped_gemm_shape(const GroupedGemm& p);
 
 // Whether a row of `cols` values is made of whole aligned groups of 16 bytes.
 bool rows_copyable(const RowsOf& o, int64_t cols, int bytes);

@@ -4,8 +4,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "common.h"
 #include "grouped.h"
+#include "grouped_stream.h"
 #include "grouped_tile.h"
 #include "vec8.h"
 
@@ -82,7 +85,45 @@ PackPlan plan_k_rows(const RowsOf& o, int64_t R, int64_t cols) {
   return q;
 }
 
+// The tile shapes and the times they are chosen by: chunk_us of one chunk (128
+// bytes of K) of a block alone on its CU, shared_us with a second block beside it,
+// end_us a block's start and end.  For y and dx fitted to 143 measured sizes (1 to
+// 2048 rows per expert, 16 to 128 experts, 512 x 256 to 4096 x 7168, bf16 and 8
+// bits): the shape taken is 1.5% from the best on average, 17% at worst.
+//   256 x 256  64 experts of 7168 x 2048 with 1024 rows each: 1.73 ms, 128 x 128
+//              2.23, 64 x 64 3.96; with 128 rows 458 us, 486, 673
+//   128 x 128  two stages, two blocks per CU: 16 experts of 2 x 1024 x 1024 with 512
+//              rows: 54 us, 256 x 256 71, 64 x 64 101
+//   64 x 64    16 experts of 1024 x 1024 with 16 rows: 11 us, 128 x 128 15, 256 x
+//              256 25
+//   32 x 128   128 experts of 512 x 512 with 4 rows: 14 us, 64 x 64 17.8, 128 x 128
+//              15.5; 64 of 7168 x 2048 with 8-bit codes: 160 us, 185, 176
+// dW's tiles of 128 and 64 rows, whose results go through LDS, end later: 64
+// experts of 7168 x 2048 with 128 rows 630 us, 128 x 128 869, 64 x 64 1927; 16 of
+// 512 x 256 with 1024 rows 33 us, 15, 13.
+struct ShapeInfo {
+  int64_t rows, cols;
+  int per_cu;
+  double chunk_us, shared_us, end_us, dw_end_us;
+};
+constexpr ShapeInfo kShapes[] = {{256, 256, 1, 1.42, 1.42, 7.0, 4.0},
+                                 {128, 128, 2, 0.40, 1.02, 2.9, 8.0},
+                                 {64, 64, 2, 0.37, 0.40, 2.8, 5.0},
+                                 {32, 128, 2, 0.41, 0.52, 2.5, 0.0}};
+constexpr int64_t kCus = 256;
+constexpr double kRead = 6.1e6, kWrite = 4.0e6;   // bytes per us of weights, of their gradients
+
+// Time of `tiles` tiles of `chunks` chunks: rounds of the card.
+double tiles_us(const ShapeInfo& s, double tiles, double chunks, double end_us) {
+  const double alone = chunks * s.chunk_us + end_us, full = chunks * s.shared_us + end_us;
+  const double slots = static_cast<double>(kCus * s.per_cu), rounds = tiles / slots;
+  if (tiles <= kCus) return alone;
+  if (rounds <= 1.0) return alone + (full - alone) * (tiles - kCus) / kCus;
+  return (rounds < 4.0 ? std::ceil(rounds) : rounds + 0.5) * full;
+}
+
 struct GroupedPlan {
+  GroupedShape shape;
   PackPlan a, b;         // b: w, or kDw's b
   uint32_t tiles_m, tiles_n;
   uint64_t tiles;        // at most
@@ -92,22 +133,46 @@ GroupedPlan make_plan(const GroupedGemm& p) {
   GroupedPlan q{};
   const int64_t R = p.groups.R, G = p.groups.n;
   const int es = p.i8 ? 1 : 2;
-  constexpr int64_t rows = 64, cols = 64;
-  if (p.kind == GroupedKind::kDw) {
+  const bool dw = p.kind == GroupedKind::kDw, dx = p.kind == GroupedKind::kDx, gated = p.kind == GroupedKind::kGated;
+  const int64_t cols = dw ? p.K : p.N * (gated ? 2 : 1);   // the tiles' columns
+  const int64_t busy = R < G ? R : G;                      // groups with rows, at most
+  // the launch's time: memory's or the tiles', whichever is longer, and some of the
+  // other.  The sizes of the groups are on the device: tiles of rows are counted
+  // as for groups of equal sizes that end anywhere in their last tile.
+  double best = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    if (dw && i == 3) break;
+    const double tn = static_cast<double>((cols + s.cols - 1) / s.cols), per_group = static_cast<double>(R) / busy;
+    double tiles, chunks, mem;
+    if (dw) {
+      tiles = static_cast<double>((p.N + s.rows - 1) / s.rows) * tn * G;
+      chunks = static_cast<double>(R) / G * 2 / kChunkBytes + 0.5;
+      mem = static_cast<double>(G) * p.N * p.K * 2 / kWrite;
+    } else {
+      const double tm = G == 1 ? static_cast<double>((R + s.rows - 1) / s.rows) : per_group / s.rows + 0.5;
+      tiles = busy * (tm > 1.0 ? tm : 1.0) * tn;
+      chunks = static_cast<double>((p.K * es + kChunkBytes - 1) / kChunkBytes);
+      mem = static_cast<double>(busy) * cols * p.K * es / kRead;
+    }
+    const double work = tiles_us(s, tiles, chunks, dw ? s.dw_end_us : s.end_us);
+    const double us = work > mem ? work + 0.2 * mem : mem + 0.2 * work;
+    if (us < best) best = us, q.shape = static_cast<GroupedShape>(i);
+  }
+  const ShapeInfo& s = kShapes[static_cast<int>(q.shape)];
+  q.tiles_n = static_cast<uint32_t>((cols + s.cols - 1) / s.cols);
+  if (dw) {
     q.a = plan_k_rows(p.a, R, p.N);
     q.b = plan_k_rows(p.b, R, p.K);
-    q.tiles_m = static_cast<uint32_t>((p.N + rows - 1) / rows);
-    q.tiles_n = static_cast<uint32_t>((p.K + cols - 1) / cols);
+    q.tiles_m = static_cast<uint32_t>((p.N + s.rows - 1) / s.rows);
     q.tiles = static_cast<uint64_t>(q.tiles_m) * q.tiles_n * G;
     return q;
   }
   q.a = plan_rows(p.a, R, p.K, es);
-  const bool dx = p.kind == GroupedKind::kDx, gated = p.kind == GroupedKind::kGated;
-  const RowsOf w{p.w, p.ldw, G * (dx ? p.K : gated ? 2 * p.N : p.N), nullptr, false};
+  const RowsOf w{p.w, p.ldw, G * (dx ? p.K : cols), nullptr, false};
   q.b = plan_rows(w, w.n, dx ? p.N : p.K, es);
-  q.tiles_n = static_cast<uint32_t>((p.N * (gated ? 2 : 1) + cols - 1) / cols);
-  const int64_t busy = R < G ? R : G;   // groups with rows; each has at most one tile that is not full
-  q.tiles = static_cast<uint64_t>((R + (rows - 1) * busy) / rows) * q.tiles_n;
+  // at most: a group with rows has at most one tile that is not full
+  q.tiles = static_cast<uint64_t>((R + (s.rows - 1) * busy) / s.rows) * q.tiles_n;
   return q;
 }
 
@@ -126,27 +191,13 @@ RowsOf packed(const RowsOf& o, const PackPlan& q, int es, void* dst) {
   return RowsOf{dst, up(q.cols * es, 16) / es, q.rows, q.gather ? nullptr : o.index, true};
 }
 
-template <Elem E, GroupedKind KIND>
-hipError_t launch_tiles(GroupedArgs t, uint64_t tiles, hipStream_t s) {
-  // a launch holds fewer than 2^32 threads
-  constexpr uint64_t kMost = 1u << 22;
-  for (uint64_t t0 = 0; t0 < tiles; t0 += kMost) {
-    const uint64_t n = tiles - t0 < kMost ? tiles - t0 : kMost;
-    t.tile0 = t0;
-    const uint64_t round = static_cast<uint64_t>(kXcds) * t.run;
-    const uint32_t grid = static_cast<uint32_t>((n + round - 1) / round * round);
-    grouped_ring_kernel<E, 32, 32, 2, 2, 4, KIND><<<grid, 256, 0, s>>>(t);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 }  // namespace
 
 bool rows_copyable(const RowsOf& o, int64_t cols, int bytes) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.ld * bytes % 16 == 0 && (cols * bytes % 16 == 0 || o.padded);
 }
+
+int grouped_gemm_shape(const GroupedGemm& p) { return static_cast<int>(make_plan(p).shape); }
 
 size_t grouped_gemm_workspace_bytes(const GroupedGemm& p) {
   if (p.groups.R == 0) return 0;
@@ -188,17 +239,14 @@ hipError_t launch_grouped_gemm(const GroupedGemm& p, hipStream_t s) {
   t.tiles_n = q.tiles_n;
   const uint64_t run = (q.tiles + kXcds - 1) / kXcds;
   t.run = static_cast<uint32_t>(run < 32 ? run : 32);
+  if (p.i8) return launch_grouped_int8(q.shape, t, q.tiles, s);
   switch (p.kind) {
-    case GroupedKind::kLinear:
-      return p.i8 ? launch_tiles<Elem::kI8, GroupedKind::kLinear>(t, q.tiles, s)
-                  : launch_tiles<Elem::kBf16, GroupedKind::kLinear>(t, q.tiles, s);
-    case GroupedKind::kGated:
-      return p.i8 ? launch_tiles<Elem::kI8, GroupedKind::kGated>(t, q.tiles, s)
-                  : launch_tiles<Elem::kBf16, GroupedKind::kGated>(t, q.tiles, s);
-    case GroupedKind::kDx: return launch_tiles<Elem::kBf16, GroupedKind::kDx>(t, q.tiles, s);
+    case GroupedKind::kLinear: return launch_grouped_tiles<Elem::kBf16, GroupedKind::kLinear>(q.shape, t, q.tiles, s);
+    case GroupedKind::kGated: return launch_grouped_tiles<Elem::kBf16, GroupedKind::kGated>(q.shape, t, q.tiles, s);
+    case GroupedKind::kDx: return launch_grouped_tiles<Elem::kBf16, GroupedKind::kDx>(q.shape, t, q.tiles, s);
     case GroupedKind::kDw: break;
   }
-  return launch_tiles<Elem::kBf16, GroupedKind::kDw>(t, q.tiles, s);
+  return launch_grouped_tiles<Elem::kBf16, GroupedKind::kDw>(q.shape, t, q.tiles, s);
 }
 
 }  // namespace dsmoe

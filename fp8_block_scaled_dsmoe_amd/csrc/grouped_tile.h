@@ -166,7 +166,7 @@ struct GroupedTile : TileCore<E, HM, HN, WM, WN, KIND == GroupedKind::kDw,
       m_end = p.N;
       const int32_t lo = __builtin_amdgcn_readfirstlane(group_begin(p.groups, group));
       const int32_t hi = max(lo, __builtin_amdgcn_readfirstlane(group_end(p.groups, group)));
-      c1 = (hi - lo + Core::kChunk - 1) / Core::kChunk;
+      c1 = static_cast<int32_t>((static_cast<uint32_t>(hi - lo) + Core::kChunk - 1) / Core::kChunk);
       a0 = SA(p.a.p, p.a.ld, m0, t.a_r, lo, hi, this->wave, this->lane);
       a1 = SA(p.a.p, p.a.ld, m0 + HM, t.a_r, lo, hi, this->wave, this->lane);
       b0 = SB(p.b.p, p.b.ld, n0, t.b_r, lo, hi, this->wave, this->lane);
@@ -250,15 +250,65 @@ struct GroupedTile : TileCore<E, HM, HN, WM, WN, KIND == GroupedKind::kDw,
   }
 };
 
+template <Elem E, int HM, int HN, int WM, int WN, GroupedKind KIND>
+__global__ __launch_bounds__(64 * WM * WN) void grouped_phased_kernel(GroupedArgs args) {
+  using T = GroupedTile<E, HM, HN, WM, WN, KIND>;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(2)];
+  T w(args, s_mem);
+  if (!w.found) return;   // the whole block
+  typename T::Acc acc;
+  phased_loop(w, acc);
+  w.finish(acc);
+}
+
 template <Elem E, int HM, int HN, int WM, int WN, int S, GroupedKind KIND>
 __global__ __launch_bounds__(64 * WM * WN) void grouped_ring_kernel(GroupedArgs args) {
   using T = GroupedTile<E, HM, HN, WM, WN, KIND>;
   __shared__ __attribute__((aligned(1024))) uint8_t s_mem[T::lds_bytes(S)];
   T w(args, s_mem);
-  if (!w.found) return;   // the whole block
+  if (!w.found) return;
   typename T::Acc acc;
   ring_loop<S>(w, acc);
   w.finish(acc);
 }
+
+// The tile shapes (grouped_gemm.hip).
+enum class GroupedShape : int { k256, k128, k64, k32x128 };
+
+// The tiles of a launch after another, which holds fewer than 2^32 threads.
+template <typename F>
+hipError_t by_tiles(GroupedArgs t, uint64_t tiles, F f) {
+  constexpr uint64_t kMost = 1u << 22;
+  const uint64_t round = static_cast<uint64_t>(kXcds) * t.run;
+  for (uint64_t t0 = 0; t0 < tiles; t0 += kMost) {
+    const uint64_t n = tiles - t0 < kMost ? tiles - t0 : kMost;
+    t.tile0 = t0;
+    f(t, static_cast<uint32_t>((n + round - 1) / round * round));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// 256 x 256 tiles: blocks that stay (grouped_stream.h) for y and dW, a block for
+// each tile for the gated product, whose longer epilogue would not stay in the
+// instruction cache (one token 200 us instead of 134; 4096 tokens to 256 experts
+// 3.30 ms instead of 3.08), and for dx, where the two are equal.
+template <Elem E, GroupedKind KIND>
+hipError_t launch_grouped_256(const GroupedArgs& t, uint64_t tiles, hipStream_t s);
+
+template <Elem E, GroupedKind KIND>
+hipError_t launch_grouped_tiles(GroupedShape shape, const GroupedArgs& t, uint64_t tiles, hipStream_t s) {
+  if (shape == GroupedShape::k256) return launch_grouped_256<E, KIND>(t, tiles, s);
+  return by_tiles(t, tiles, [&](const GroupedArgs& q, uint32_t grid) {
+    if (shape == GroupedShape::k128)
+      grouped_ring_kernel<E, 64, 64, 2, 4, 2, KIND><<<grid, 512, 0, s>>>(q);
+    else if (shape == GroupedShape::k64 || KIND == GroupedKind::kDw)
+      grouped_ring_kernel<E, 32, 32, 2, 2, 4, KIND><<<grid, 256, 0, s>>>(q);
+    else if constexpr (KIND != GroupedKind::kDw)
+      grouped_ring_kernel<E, 16, 64, 1, 4, 4, KIND><<<grid, 256, 0, s>>>(q);
+  });
+}
+hipError_t launch_grouped_int8(GroupedShape shape, const GroupedArgs& t, uint64_t tiles, hipStream_t s);
 
 }  // namespace dsmoe

@@ -30,6 +30,7 @@
 namespace dsmoe {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -122,13 +123,19 @@ struct Half {
 // (Masking every copy by its k, and a range computed anew per chunk, cost the
 // multiplies of a one-wave-per-SIMD loop 8 to 10 cycles per vector
 // instruction.)
-// WAIT: see copy().
-template <Elem E, int HR, bool KROWS, int NW, bool WAIT>
+// WAIT: see copy().  PAIR: 0, or the half holds every other run of PAIR rows, from
+// its first row on (both halves then lie side by side, run by run).
+template <Elem E, int HR, bool KROWS, int NW, bool WAIT, int PAIR = 0>
 struct Source {
   using H = Half<HR, KROWS, NW>;
   static constexpr int ES = ElemOf<E>::kBytes;
   static constexpr int kChunk = kChunkBytes / ES;   // K per chunk
   static_assert(!KROWS || E == Elem::kBf16, "integers are row operands");
+  static constexpr int kSpan = PAIR ? 2 * HR - PAIR : HR;   // rows from the first to past the last
+  static __device__ __forceinline__ int place(int r) {
+    if constexpr (PAIR > 0) return r / PAIR * (2 * PAIR) + r % PAIR;
+    return r;
+  }
   uint64_t base;                  // byte address of the half's (row 0, chunk's first k)
   int32_t range;                  // bytes from base that may be read
   uint32_t ld2;                   // row stride in bytes
@@ -138,11 +145,11 @@ struct Source {
   uint32_t voff[H::kCopies];
 
   __device__ __forceinline__ Source() {}
-  // rows [r0, r0 + HR) of `rows` rows at p, chunks from k0 on, k_end: end of valid k
+  // rows from r0 on of `rows` rows at p, chunks from k0 on, k_end: end of valid k
   __device__ __forceinline__ Source(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k_end,
                                     int wave, int lane) {
     ld2 = static_cast<uint32_t>(ld * ES);
-    const int64_t left = min(static_cast<int64_t>(HR), rows - r0);
+    const int64_t left = min(static_cast<int64_t>(kSpan), rows - r0);
     k_left = left > 0 ? static_cast<int32_t>(k_end - k0) : 0;
     lane_k = 16 / ES * ((lane & 7) ^ (lane >> 3));
     if constexpr (KROWS) {
@@ -158,10 +165,10 @@ struct Source {
       const int j = H::index(wave, i);
       if constexpr (KROWS) {
         const int k = (j * 64 + lane) / H::kSegs, seg = (j * 64 + lane) % H::kSegs;
-        const int col = ((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8;
+        const int col = place(((seg >> 1) ^ H::key(k)) * 16 + (seg & 1) * 8);
         voff[i] = col < left ? static_cast<uint32_t>(k) * ld2 + col * 2 : kOutside;
       } else {
-        voff[i] = static_cast<uint32_t>(8 * j + lane / 8) * ld2 + ES * lane_k;
+        voff[i] = static_cast<uint32_t>(place(8 * j + lane / 8)) * ld2 + ES * lane_k;
       }
     }
     if (k_left < kChunk) cut();
@@ -171,7 +178,7 @@ struct Source {
   // zeros).  n * ld * ES < 2^31.
   __device__ __forceinline__ Source(const void* p, int64_t ld, int32_t n, const int32_t* index, int64_t left, int64_t k0,
                                     int64_t k_end, int wave, int lane) {
-    static_assert(!KROWS, "row operands");
+    static_assert(!KROWS && PAIR == 0, "row operands, one after the other");
     ld2 = static_cast<uint32_t>(ld * ES);
     k_left = left > 0 ? static_cast<int32_t>(k_end - k0) : 0;
     lane_k = 16 / ES * ((lane & 7) ^ (lane >> 3));
@@ -186,7 +193,7 @@ struct Source {
     }
     if (k_left < kChunk) cut();
   }
-  // past every range (the largest is 128 rows of 2^23 bytes, or 2^31 - 1 by index)
+  // past every range (the largest is 224 rows of 2^23 bytes, or 2^31 - 1 by index)
   static constexpr uint32_t kOutside = 0x80000000u;
   // The last chunk, and those past the end: what is past k_left reads as zero.
   __device__ __forceinline__ void cut() {
@@ -265,7 +272,8 @@ struct Reader {
 // What a block and its waves work on.  HM, HN: rows of a half of A and of B;
 // WM x WN waves.  GATED: half 0 of B holds gate rows, half 1 the same up
 // rows, so a lane has both sums of its columns.
-template <Elem E, int HM, int HN, int WM, int WN, bool AT, bool BT, bool GATED, bool WAIT>
+// WAIT and PAIR (of B): see Source.
+template <Elem E, int HM, int HN, int WM, int WN, bool AT, bool BT, bool GATED, bool WAIT, int PAIR = 0>
 struct TileCore {
   static constexpr bool kGated = GATED;
   static constexpr int NW = WM * WN;
@@ -274,7 +282,7 @@ struct TileCore {
   using El = ElemOf<E>;
   using Frag = typename El::Frag;
   using SA = Source<E, HM, AT, NW, WAIT>;
-  using SB = Source<E, HN, BT, NW, WAIT>;
+  using SB = Source<E, HN, BT, NW, WAIT, PAIR>;
   static constexpr int LA = SA::H::kCopies, LB = SB::H::kCopies;
   static constexpr int AB = SA::H::kBytes, BB = SB::H::kBytes;
   // a stage of LDS and the places of the halves in it

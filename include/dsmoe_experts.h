@@ -29,7 +29,8 @@
  *   An index outside [0, n) reads as a row of zeros.
  * - Weights of G experts are one matrix of all their rows, expert by expert.
  * - Sizes: 1 <= G <= DSMOE_MAX_EXPERTS; row lengths and row strides are in [1,
- *   DSMOE_DENSE_MAX_DIM]; R and n in [0, 2^31), n > 0 where R > 0.  No rows:
+ *   DSMOE_DENSE_MAX_DIM]; R and n in [0, 2^31), n > 0 where R > 0; the weights and
+ *   either side's R rows have at most 2^40 elements.  No rows:
  *   outputs per row are not touched, weight gradients are written as 0.
  * - The workspace is 256-byte aligned; its size comes from the
  *   ..._workspace_bytes call with the same arguments (0: NULL is accepted).

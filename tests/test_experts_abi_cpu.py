@@ -200,6 +200,37 @@ def test_weights_of_experts_are_rows_of_one_matrix(d):
         take(w.float())
 
 
+def test_sizes_that_run_every_grouped_kernel(d):
+    """Each size of grouped_kernels.SIZES takes the kernel that its GPU test is there
+    for, and together they are every tile shape of every product."""
+    import grouped_kernels as gk
+    for size, want in gk.SIZES.items():
+        assert gk.shape(d.lib, *size) == want, size
+        s = gk.group_sizes(size[1], size[2])
+        assert len(s) == size[1] and sum(s) == size[2] and min(s) >= 0
+    for product in gk.PRODUCTS:
+        shapes = {s for k, s in gk.SIZES.items() if k[0] == product}
+        assert shapes == set(gk.SHAPES) - ({"32x128"} if product == "dw" else set()), product
+    assert gk.shape(d.lib, "y", 0, 8, 8, 8) is None and gk.shape(d.lib, "y", 1, 0, 8, 8) is None
+    # what sizes of the framework take
+    assert gk.shape(d.lib, "gated", 256, 8, 2048, 7168) == "64x64"
+    assert gk.shape(d.lib, "y", 256, 512, 7168, 2048) == "32x128"
+    assert gk.shape(d.lib, "gated", 256, 32768, 2048, 7168) == "256x256"
+    assert gk.shape(d.lib, "dw", 32, 16384, 4096, 7168) == "256x256"
+
+
+def test_sizes_past_the_card_are_refused(d):
+    """Numbers of elements past 2^40, whose tiles would not be counted in 32 bits."""
+    big = dict(ldx=4194304, ldw=4194304, ldy=4194304)
+    assert _linear(d, N=4194304, K=4194304, **big) == SHAPE
+    assert _linear(d, N=4194304, K=64, R=(1 << 31) - 1, n=(1 << 31) - 1, **big) == SHAPE
+    assert _int8(d, N=4194304, K=131071, G=1024, **big) == SHAPE
+    assert _gated(d, I=2097152, H=4194304, **big) == SHAPE
+    wide = dict(lddy=4194304, ldx=4194304, ldw=4194304, lddx=4194304, lddw=4194304)
+    assert _linear_bwd(d, N=4194304, K=4194304, **wide) == SHAPE
+    assert d.lib.dsmoe_grouped_linear_workspace_bytes(A, 4194304, 4, None, A, 4194304, 2, 4, 4194304, 4194304) == 0
+
+
 C_PROGRAM = r"""
 #include <stdio.h>
 #include "dsmoe_experts.h"
