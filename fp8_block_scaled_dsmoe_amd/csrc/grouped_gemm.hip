@@ -24,10 +24,14 @@ struct PackArgs {
   const int32_t* index;
   int64_t ld, rows, cols, n;   // ld, cols in bytes
 };
-__global__ __launch_bounds__(256) void pack_grouped_kernel(PackArgs a) {
+// Both operands of a product in one launch: blocks [0, blocks0) copy the first, the
+// others the second.
+__global__ __launch_bounds__(256) void pack_grouped_kernel(PackArgs first, PackArgs second, uint32_t blocks0) {
+  const bool one = blockIdx.x < blocks0;
+  const PackArgs a = one ? first : second;
+  const uint32_t block = one ? blockIdx.x : blockIdx.x - blocks0, blocks = one ? blocks0 : gridDim.x - blocks0;
   const int64_t segs = (a.cols + 15) / 16, all = a.rows * segs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
+  for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(blocks) * 256) {
     const int64_t r = i >> 32 ? i / segs : static_cast<uint32_t>(i) / static_cast<uint32_t>(segs);
     const int64_t c = (i - r * segs) * 16;
     const int64_t row = a.index ? a.index[r] : r;
@@ -176,13 +180,18 @@ GroupedPlan make_plan(const GroupedGemm& p) {
   return q;
 }
 
-hipError_t pack(const RowsOf& o, const PackPlan& q, int es, void* dst, hipStream_t s) {
-  const int64_t ld = up(q.cols * es, 16), all = q.rows * (ld / 16);
-  if (all == 0) return hipSuccess;
-  const int64_t blocks = (all + 255) / 256;
-  pack_grouped_kernel<<<static_cast<uint32_t>(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(
-      PackArgs{static_cast<const char*>(o.p), static_cast<char*>(dst), q.gather ? o.index : nullptr, o.ld * es, q.rows,
-               q.cols * es, o.n});
+PackArgs pack_args(const RowsOf& o, const PackPlan& q, int es, void* dst) {
+  return PackArgs{static_cast<const char*>(o.p), static_cast<char*>(dst), q.gather ? o.index : nullptr, o.ld * es,
+                  q.pack ? q.rows : 0, q.cols * es, o.n};
+}
+uint32_t pack_blocks(const PackArgs& a) {
+  const int64_t blocks = (a.rows * ((a.cols + 15) / 16) + 255) / 256;
+  return static_cast<uint32_t>(blocks < 8192 ? blocks : 8192);
+}
+hipError_t pack(const PackArgs& a, const PackArgs& b, hipStream_t s) {
+  const uint32_t na = pack_blocks(a), nb = pack_blocks(b);
+  if (na + nb == 0) return hipSuccess;
+  pack_grouped_kernel<<<na + nb, 256, 0, s>>>(a, b, na);
   return hipGetLastError();
 }
 
@@ -212,17 +221,16 @@ hipError_t launch_grouped_gemm(const GroupedGemm& p, hipStream_t s) {
   GroupedArgs t{};
   t.p = p;
   t.scale_index = p.a.index, t.scale_n = p.a.n;
-  char* ws = static_cast<char*>(p.workspace);
-  hipError_t e = hipSuccess;
-  if (q.a.pack) {
-    if ((e = pack(p.a, q.a, es, ws, s)) != hipSuccess) return e;
-    t.p.a = packed(p.a, q.a, es, ws);
-  }
+  char* const to_a = static_cast<char*>(p.workspace);
+  char* const to_b = to_a + q.a.bytes;
+  const RowsOf b = dw ? p.b : RowsOf{p.w, p.ldw, q.b.rows, nullptr, false};
+  PackPlan copy_b = q.b;
+  copy_b.pack = q.b.pack && !p.add;   // the product that is added finds it there
+  const hipError_t e = pack(pack_args(p.a, q.a, es, to_a), pack_args(b, copy_b, es, to_b), s);
+  if (e != hipSuccess) return e;
+  if (q.a.pack) t.p.a = packed(p.a, q.a, es, to_a);
   if (q.b.pack) {
-    const RowsOf b = dw ? p.b : RowsOf{p.w, p.ldw, q.b.rows, nullptr, false};
-    char* to = ws + q.a.bytes;
-    if ((e = pack(b, q.b, es, to, s)) != hipSuccess) return e;
-    const RowsOf c = packed(b, q.b, es, to);
+    const RowsOf c = packed(b, q.b, es, to_b);
     if (dw)
       t.p.b = c;
     else
