@@ -126,6 +126,8 @@ struct Stream : StreamCore<E, HM, HN, WM, WN, KIND> {
       local = tile - static_cast<uint32_t>(f0) * t.tiles_n;
       rows = static_cast<uint32_t>(f1 - f0);
     }
+    // past the group only where offsets that break the rule let a count wrap
+    if (local >= rows * t.tiles_n) return false;
     const int32_t lo = __builtin_amdgcn_readfirstlane(table.begin[d.group]);
     const int32_t hi = __builtin_amdgcn_readfirstlane(table.end[d.group]);
     const uint32_t per_band = kBand * t.tiles_n, band = local / per_band, in = local - band * per_band;

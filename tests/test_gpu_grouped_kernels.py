@@ -92,3 +92,49 @@ def test_grouped_kernel(d, size):
         else:
             y = d.int8_linear(x, xs, w, ws, doff, drows, y=_nan(R, N, out, pad=5))
             _check_rows(y, want, 3.01 * U * np.abs(want), off, out, out)
+
+
+# of SIZES, one of each product in 256 x 256 tiles and one in small ones
+BROKEN = [("y", 130, 39000, 136, 72), ("y", 3, 65, 1000, 520), ("dx", 40, 12000, 72, 520), ("dw", 700, 14000, 264, 300),
+          ("dw", 7, 5000, 520, 391), ("gated", 40, 5200, 520, 201), ("int8", 130, 39000, 136, 200)]
+
+
+@pytest.mark.parametrize("size", BROKEN, ids=lambda s: "-".join(map(str, s)))
+def test_offsets_that_break_the_rule(d, size):
+    """Offsets that fall, that are negative or that pass R: nothing outside the result
+    is written (bands of NaN on both sides), and the next call is right."""
+    product, G, R, N, K = size
+    r = np.random.default_rng(R)
+    banner(f"{product} {G} groups {R} rows {N}x{K}: offsets that break the rule")
+    bad = r.integers(-R, 2 * R, G + 1)
+    bad[r.integers(0, G + 1, G // 3 + 1)] = R
+    cases = [bad, bad[::-1].copy(), np.full(G + 1, -2 ** 31), np.full(G + 1, 2 ** 31 - 1),
+             np.where(np.arange(G + 1) % 2, R, 0)]
+    good = gk.group_sizes(G, R)
+    cols = {"y": N, "dx": K, "dw": K, "gated": N, "int8": N}[product]
+    rows = G * N if product == "dw" else R
+    guard = 300
+    buf = _nan(rows + 2 * guard, cols)
+    out = buf[guard:guard + rows]
+    if product == "int8":
+        x, w = _codes(r, R, K)[0], _codes(r, G, N, K)[0]
+        (xs, _), (ws, _) = _scales(r, R), _scales(r, G, N)
+        run = lambda off: d.int8_linear(x, xs, w, ws, off, y=out)
+    elif product == "dw":
+        dy, x, w = _mat(r, R, N)[0], _mat(r, R, K)[0], _experts(r, G, N, K)[0]
+        run = lambda off: d.grouped_linear_backward(dy, x, w, off, need_dx=False, dw=out.unflatten(0, (G, N)))
+    elif product == "dx":
+        dy, x, w = _mat(r, R, N)[0], _mat(r, R, K)[0], _experts(r, G, N, K)[0]
+        run = lambda off: d.grouped_linear_backward(dy, x, w, off, need_dw=False, dx=out)
+    else:
+        x, w = _mat(r, R, K)[0], _experts(r, G, N * (2 if product == "gated" else 1), K)[0]
+        run = (lambda off: d.grouped_linear(x, w, off, y=out)) if product == "y" else \
+            (lambda off: d.grouped_gated_linear(x, w, off, a=out))
+    run(_offsets(good)[1])
+    want = out.clone()
+    for c in cases:
+        run(_i32(c))
+        torch.cuda.synchronize()
+        assert torch.isnan(buf[:guard]).all() and torch.isnan(buf[guard + rows:]).all()
+    run(_offsets(good)[1])
+    assert torch.equal(out, want)
