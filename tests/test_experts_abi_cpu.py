@@ -231,6 +231,24 @@ def test_sizes_past_the_card_are_refused(d):
     assert d.lib.dsmoe_grouped_linear_workspace_bytes(A, 4194304, 4, None, A, 4194304, 2, 4, 4194304, 4194304) == 0
 
 
+def test_tokens_of_the_pass_are_the_routing_s(d):
+    i32, b16 = torch.int32, torch.bfloat16
+    routing = {"offsets": torch.zeros(3, dtype=i32), "perm": torch.zeros(8, dtype=i32),
+               "inv": torch.zeros((4, 2), dtype=i32), "gates": torch.zeros((4, 2))}
+    w13, w2 = torch.zeros((2, 16, 8), dtype=b16), torch.zeros((2, 8, 8), dtype=b16)
+    x, short = torch.zeros((4, 8), dtype=b16), torch.zeros((3, 8), dtype=b16)
+    with pytest.raises(ValueError, match="tokens"):
+        d.moe_ffn_forward(short, routing, w13, w2)
+    with pytest.raises(ValueError, match="tokens"):
+        d.moe_ffn_int8_forward(short, routing, (w13, None), (w2, None))
+    with pytest.raises(ValueError, match="n_shared"):
+        d.moe_ffn_forward(x, routing, w13, w2, n_shared=2)
+    saved = {"offsets": routing["offsets"], "perm": routing["perm"], "scale": None, "shared0": -1, "a": None, "h": None}
+    for dy, y in ((short, x), (short, short)):
+        with pytest.raises(ValueError, match="routing"):
+            d.moe_ffn_backward(dy, y, routing, w13, w2, saved)
+
+
 C_PROGRAM = r"""
 #include <stdio.h>
 #include "dsmoe_experts.h"
