@@ -361,7 +361,13 @@ def int8_gated_linear(x: torch.Tensor, x_scale: torch.Tensor, w13: torch.Tensor,
     return a
 
 
-def _routed_rows(x, routing, n_shared):
+def _tokens(x, routing):
+    """x and the routing are of the same tokens."""
+    if x.shape[0] != routing["inv"].shape[0]:
+        raise ValueError(f"x has {x.shape[0]} tokens, the routing {routing['inv'].shape[0]}")
+
+
+def _routed_rows(routing, n_shared):
     """(offsets, tokens of the rows, gates of the rows, first shared row or -1):
     the routed rows and, with a shared expert, one more group of every token
     with gate 1."""
@@ -369,8 +375,6 @@ def _routed_rows(x, routing, n_shared):
         raise ValueError("n_shared must be 0 or 1")
     off, perm, inv, gates = (routing[k] for k in ("offsets", "perm", "inv", "gates"))
     T, routed = inv.shape[0], perm.numel()
-    if x.shape[0] != T:
-        raise ValueError(f"x has {x.shape[0]} tokens, the routing {T}")
     scale = torch.ones((routed + n_shared * T,), dtype=torch.float32, device=perm.device)
     scale[inv.reshape(-1).long()] = gates.reshape(-1)
     if n_shared:
@@ -390,7 +394,8 @@ def moe_ffn_forward(x: torch.Tensor, routing: dict, w13: torch.Tensor, w2: torch
     [E][H][I], with n_shared = 1 one more expert that every token takes with
     gate 1.  H is a multiple of 8.  Returns (y, saved): y bf16 [T][H] and, when
     training, what moe_ffn_backward needs."""
-    off, perm, scale, shared0 = _routed_rows(x, routing, n_shared)
+    off, perm, scale, shared0 = _routed_rows(routing, n_shared)
+    _tokens(x, routing)
     a, h = grouped_gated_linear(x, w13, off, act, rows=perm, row_scale=scale, save_h=training)
     o = grouped_linear(a, w2, off)
     y = combine_rows(o, routing["inv"], shared0)
@@ -421,7 +426,8 @@ def moe_ffn_int8_forward(x: torch.Tensor, routing: dict, w13: tuple, w2: tuple, 
     """moe_ffn_forward on 8-bit integers: w13 and w2 are (codes, scales) of the
     experts' weights as from quant_rows_int8; x and the activations are
     quantised per row on the way.  x bf16 [T][H]; returns y bf16 [T][H]."""
-    off, perm, scale, shared0 = _routed_rows(x, routing, n_shared)
+    off, perm, scale, shared0 = _routed_rows(routing, n_shared)
+    _tokens(x, routing)
     q, s = quant_rows_int8(x)
     a = int8_gated_linear(q, s, *w13, off, act, rows=perm, row_scale=scale)
     q, s = quant_rows_int8(a)

@@ -138,3 +138,50 @@ def test_offsets_that_break_the_rule(d, size):
         assert torch.isnan(buf[:guard]).all() and torch.isnan(buf[guard + rows:]).all()
     run(_offsets(good)[1])
     assert torch.equal(out, want)
+
+
+def test_blocks_that_stay_in_graphs_and_on_two_streams(d):
+    """y, dW and the 8-bit y in 256 x 256 tiles, several tiles a block: captured
+    together and replayed with other inputs and other offsets, eager work in
+    between; and on two streams at once."""
+    G, R, N, K = 40, 12000, 520, 520
+    assert all(gk.shape(d.lib, p, G, R, N, K) == "256x256" for p in ("y", "dw"))
+    G8, R8, N8, K8 = 130, 39000, 136, 200
+    assert gk.shape(d.lib, "int8", G8, R8, N8, K8) == "256x256"
+    banner("grouped 256x256 in graphs and on two streams")
+    r = np.random.default_rng(5)
+    sets = []
+    for i in range(2):
+        sizes = gk.group_sizes(G, R)
+        r.shuffle(sizes)
+        sets.append([_mat(r, R, K)[0], _mat(r, R, N, 0.1)[0], _experts(r, G, N, K)[0], _offsets(sizes)[1],
+                     _codes(r, R8, K8)[0], _scales(r, R8)[0], _codes(r, G8, N8, K8)[0], _scales(r, G8, N8)[0],
+                     _offsets(gk.group_sizes(G8, R8))[1]])
+
+    def step(x, dy, w, off, q, qs, w8, w8s, off8):
+        y = d.grouped_linear(x, w, off)
+        dw = d.grouped_linear_backward(dy, x, w, off, need_dx=False)[1]
+        return y, dw, d.int8_linear(q, qs, w8, w8s, off8)
+
+    want = [step(*s) for s in sets]
+    held = [t.clone() for t in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*held)
+    for i in (0, 1, 0):
+        for t, s in zip(held, sets[i]):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i])), i
+        assert all(torch.equal(a, b) for a, b in zip(step(*sets[1 - i]), want[1 - i]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(*sets[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
