@@ -92,9 +92,10 @@ PackPlan plan_k_rows(const RowsOf& o, int64_t R, int64_t cols) {
 
 // The tile shapes and the times they are chosen by: chunk_us of one chunk (128
 // bytes of K) of a block alone on its CU, shared_us with a second block beside it,
-// end_us a block's start and end.  For y and dx fitted to 143 measured sizes (1 to
-// 2048 rows per expert, 16 to 128 experts, 512 x 256 to 4096 x 7168, bf16 and 8
-// bits): the shape taken is 1.5% from the best on average, 17% at worst.
+// end_us a block's start and end.  For y, and dx in whole tiles, fitted to 143
+// measured sizes (1 to 2048 rows per expert, 16 to 128 experts, 512 x 256 to 4096 x
+// 7168, bf16 and 8 bits): the shape taken is 1.5% from the best on average, 17% at
+// worst.
 //   256 x 256  64 experts of 7168 x 2048 with 1024 rows each: 1.73 ms, 128 x 128
 //              2.23, 64 x 64 3.96; with 128 rows 458 us, 486, 673
 //   128 x 128  two stages, two blocks per CU: 16 experts of 2 x 1024 x 1024 with 512
@@ -115,6 +116,18 @@ constexpr ShapeInfo kShapes[] = {{256, 256, 1, 1.42, 1.42, 7.0, 4.0},
                                  {128, 128, 2, 0.40, 1.02, 2.9, 8.0},
                                  {64, 64, 2, 0.37, 0.40, 2.8, 5.0},
                                  {32, 128, 2, 0.41, 0.52, 2.5, 0.0}};
+// The gated product and dx compute a 256-row tile of few rows in 1/2 or 3/4 of the
+// height (grouped_tile.h), and their kernel takes longer to start and end: up to
+// `rows` rows a chunk takes chunk_us.  Fitted to 108 measured sizes (16 to 320 rows
+// per expert, 16 and 64 experts, 1024 x 512 to 7168 x 2048, bf16 and 8 bits): the
+// shape taken is 1.0% from the best on average, 20% at worst (16 rows of 2048 x 1024,
+// 29 us); by whole tiles' times 3.9%, 52% at worst.  64 experts of 7168 x 2048 with 48
+// rows, dx: 647 us, 128 x 128 677, 64 x 64 883; with 96 rows gated 653 us, 768, 1047.
+struct ShortTile {
+  double rows, chunk_us;
+};
+constexpr ShortTile kShort[] = {{128, 0.8}, {192, 1.1}};
+constexpr double kShortEnd = 9.0;
 constexpr int64_t kCus = 256;
 constexpr double kRead = 6.1e6, kWrite = 4.0e6;   // bytes per us of weights, of their gradients
 
@@ -146,7 +159,7 @@ GroupedPlan make_plan(const GroupedGemm& p) {
   // as for groups of equal sizes that end anywhere in their last tile.
   double best = 1e300;
   for (int i = 0; i < 4; ++i) {
-    const ShapeInfo& s = kShapes[i];
+    ShapeInfo s = kShapes[i];
     if (dw && i == 3) break;
     const double tn = static_cast<double>((cols + s.cols - 1) / s.cols), per_group = static_cast<double>(R) / busy;
     double tiles, chunks, mem;
@@ -155,7 +168,16 @@ GroupedPlan make_plan(const GroupedGemm& p) {
       chunks = static_cast<double>(R) / G * 2 / kChunkBytes + 0.5;
       mem = static_cast<double>(G) * p.N * p.K * 2 / kWrite;
     } else {
-      const double tm = G == 1 ? static_cast<double>((R + s.rows - 1) / s.rows) : per_group / s.rows + 0.5;
+      double tm = G == 1 ? static_cast<double>((R + s.rows - 1) / s.rows) : per_group / s.rows + 0.5;
+      if (i == 0 && (gated || dx)) {
+        s.end_us = kShortEnd;
+        for (const ShortTile& t : kShort) {
+          if (per_group > t.rows) continue;
+          s.chunk_us = s.shared_us = t.chunk_us;
+          tm = 1.0;
+          break;
+        }
+      }
       tiles = busy * (tm > 1.0 ? tm : 1.0) * tn;
       chunks = static_cast<double>((p.K * es + kChunkBytes - 1) / kChunkBytes);
       mem = static_cast<double>(busy) * cols * p.K * es / kRead;

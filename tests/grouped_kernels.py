@@ -11,6 +11,7 @@ PRODUCTS = ("y", "dx", "dw", "gated", "int8", "int8 gated")   # N, K of linear; 
 
 # (product, groups, rows, N, K): shape.  256 x 256 tiles of y and dw by blocks that
 # stay: one tile a block, several of one chunk, of two and of many, wide and ragged.
+# Those of dx and gated have last tiles of every height.
 SIZES = {
     ("y", 1, 5, 72, 72): "32x128",
     ("y", 7, 900, 1000, 201): "32x128",
@@ -24,7 +25,7 @@ SIZES = {
     ("dx", 1, 3, 72, 72): "32x128",
     ("dx", 3, 65, 520, 72): "64x64",
     ("dx", 300, 12000, 72, 72): "128x128",
-    ("dx", 40, 12000, 72, 520): "256x256",
+    ("dx", 40, 12000, 520, 520): "256x256",
     ("dx", 21, 9001, 500, 1033): "256x256",
     ("dw", 1, 1, 72, 72): "256x256",
     ("dw", 700, 14000, 264, 300): "256x256",
@@ -45,7 +46,7 @@ SIZES = {
     ("int8 gated", 1, 5, 72, 72): "32x128",
     ("int8 gated", 40, 5200, 136, 72): "64x64",
     ("int8 gated", 130, 9100, 72, 72): "128x128",
-    ("int8 gated", 40, 5200, 520, 200): "256x256",
+    ("int8 gated", 40, 5200, 520, 520): "256x256",
     ("int8 gated", 40, 5200, 521, 1100): "256x256",
 }
 

@@ -95,7 +95,7 @@ def test_grouped_kernel(d, size):
 
 
 # of SIZES, one of each product in 256 x 256 tiles and one in small ones
-BROKEN = [("y", 130, 39000, 136, 72), ("y", 3, 65, 1000, 520), ("dx", 40, 12000, 72, 520), ("dw", 700, 14000, 264, 300),
+BROKEN = [("y", 130, 39000, 136, 72), ("y", 3, 65, 1000, 520), ("dx", 40, 12000, 520, 520), ("dw", 700, 14000, 264, 300),
           ("dw", 7, 5000, 520, 391), ("gated", 40, 5200, 520, 201), ("int8", 130, 39000, 136, 200)]
 
 
