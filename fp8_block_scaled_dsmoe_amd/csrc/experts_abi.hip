@@ -164,7 +164,8 @@ size_t linear_bytes(bool i8, bool gated, const void* x, int64_t ldx, int64_t n, 
 extern "C" {
 
 // Not part of the interface: lets tests hold the sizes they use to the kernels
-// they are for.  The tile shape (0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 32 x 128)
+// they are for.  The tile shape (0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 32 x 128,
+// 4: 256 x 256 where y takes a block for each tile instead of blocks that stay)
 // of R aligned rows in G groups: product 0 y of dsmoe_grouped_linear, 1 its dx, 2
 // its dw (N, K as there), 3 dsmoe_grouped_gated_linear (N its I, K its H), 4 and 5
 // the 8-bit forms of 0 and 3.

@@ -57,7 +57,8 @@ struct GroupedGemm {
 };
 size_t grouped_gemm_workspace_bytes(const GroupedGemm& p);
 hipError_t launch_grouped_gemm(const GroupedGemm& p, hipStream_t s);
-// The tile shape that a product takes (the index in kShapes).
+// The tile shape that a product takes (the index in kShapes; 4: the first, y by a
+// block for each tile).
 int grouped_gemm_shape(const GroupedGemm& p);
 
 // Whether a row of `cols` values is made of whole aligned groups of 16 bytes.

@@ -116,17 +116,23 @@ constexpr ShapeInfo kShapes[] = {{256, 256, 1, 1.42, 1.42, 7.0, 4.0},
                                  {128, 128, 2, 0.40, 1.02, 2.9, 8.0},
                                  {64, 64, 2, 0.37, 0.40, 2.8, 5.0},
                                  {32, 128, 2, 0.41, 0.52, 2.5, 0.0}};
-// The gated product and dx compute a 256-row tile of few rows in 1/2 or 3/4 of the
-// height (grouped_tile.h), and their kernel takes longer to start and end: up to
-// `rows` rows a chunk takes chunk_us.  Fitted to 108 measured sizes (16 to 320 rows
-// per expert, 16 and 64 experts, 1024 x 512 to 7168 x 2048, bf16 and 8 bits): the
-// shape taken is 1.0% from the best on average, 20% at worst (16 rows of 2048 x 1024,
-// 29 us); by whole tiles' times 3.9%, 52% at worst.  64 experts of 7168 x 2048 with 48
-// rows, dx: 647 us, 128 x 128 677, 64 x 64 883; with 96 rows gated 653 us, 768, 1047.
+// A block for each 256-row tile computes one of few rows in 1/2 or 3/4 of the height
+// (grouped_tile.h) and takes longer to start and end: with up to `rows` rows per
+// group, a tile each, a chunk takes chunk_us.  For the gated product and dx fitted
+// to 108 measured sizes (16 to 320 rows per expert, 16 and 64 experts, 1024 x 512 to
+// 7168 x 2048, bf16 and 8 bits): the shape taken is 1.0% from the best on average,
+// 20% at worst (16 rows of 2048 x 1024, 29 us); by whole tiles' times 3.9%, 52% at
+// worst.  64 experts of 7168 x 2048 with 48 rows, dx: 647 us, 128 x 128 677, 64 x 64
+// 883; with 96 rows gated 653 us, 768, 1047.
+// y takes these blocks up to the last entry's rows, past it those that stay
+// (grouped_stream.h): 256 experts of 7168 x 2048 with 128 rows 1.67 ms, 1.73 by blocks
+// that stay, in 8 bits 0.91, 0.99; with 192 rows 1.83, 1.82 and 1.07, 1.07; with 224
+// 1.95, 1.87 and 1.15, 1.11; with 256 2.43, 2.36 and 1.47, 1.41.  64 of 1024 x 512 with
+// 192 rows 25 us, 31 and 22, 28; with 224 26, 31 and 23, 29; with 256 45, 45.
 struct ShortTile {
   double rows, chunk_us;
 };
-constexpr ShortTile kShort[] = {{128, 0.8}, {192, 1.1}};
+constexpr ShortTile kShort[] = {{128, 0.8}, {192, 1.1}, {224, 1.42}};
 constexpr double kShortEnd = 9.0;
 constexpr int64_t kCus = 256;
 constexpr double kRead = 6.1e6, kWrite = 4.0e6;   // bytes per us of weights, of their gradients
@@ -142,6 +148,7 @@ double tiles_us(const ShapeInfo& s, double tiles, double chunks, double end_us) 
 
 struct GroupedPlan {
   GroupedShape shape;
+  bool few_rows;         // per group: a block for each 256-row tile, of less height
   PackPlan a, b;         // b: w, or kDw's b
   uint32_t tiles_m, tiles_n;
   uint64_t tiles;        // at most
@@ -169,8 +176,9 @@ GroupedPlan make_plan(const GroupedGemm& p) {
       mem = static_cast<double>(G) * p.N * p.K * 2 / kWrite;
     } else {
       double tm = G == 1 ? static_cast<double>((R + s.rows - 1) / s.rows) : per_group / s.rows + 0.5;
-      if (i == 0 && (gated || dx)) {
-        s.end_us = kShortEnd;
+      if (i == 0) {
+        q.few_rows = per_group <= kShort[2].rows;
+        if (gated || dx || q.few_rows) s.end_us = kShortEnd;
         for (const ShortTile& t : kShort) {
           if (per_group > t.rows) continue;
           s.chunk_us = s.shared_us = t.chunk_us;
@@ -229,7 +237,11 @@ bool rows_copyable(const RowsOf& o, int64_t cols, int bytes) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.ld * bytes % 16 == 0 && (cols * bytes % 16 == 0 || o.padded);
 }
 
-int grouped_gemm_shape(const GroupedGemm& p) { return static_cast<int>(make_plan(p).shape); }
+int grouped_gemm_shape(const GroupedGemm& p) {
+  const GroupedPlan q = make_plan(p);
+  const bool each = q.shape == GroupedShape::k256 && p.kind == GroupedKind::kLinear && q.few_rows;
+  return each ? 4 : static_cast<int>(q.shape);
+}
 
 size_t grouped_gemm_workspace_bytes(const GroupedGemm& p) {
   if (p.groups.R == 0) return 0;
@@ -267,6 +279,7 @@ hipError_t launch_grouped_gemm(const GroupedGemm& p, hipStream_t s) {
   t.b_r = dw ? up(p.K, per16) : dx ? up(p.N, per16) : p.N;
   t.chunks = static_cast<int32_t>((p.K * es + kChunkBytes - 1) / kChunkBytes);
   t.tiles_m = q.tiles_m;
+  t.few_rows = q.few_rows;
   t.tiles_n = q.tiles_n;
   const uint64_t run = (q.tiles + kXcds - 1) / kXcds;
   t.run = static_cast<uint32_t>(run < 32 ? run : 32);

@@ -501,14 +501,18 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_stream_kernel(GroupedArg
 template <Elem E, GroupedKind KIND>
 hipError_t launch_grouped_256(const GroupedArgs& t, uint64_t tiles, hipStream_t s) {
   if constexpr (KIND == GroupedKind::kLinear || KIND == GroupedKind::kDw) {
-    const uint32_t grid = static_cast<uint32_t>(tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256);   // of 256 CUs
-    grouped_stream_kernel<E, 128, 128, 2, 4, KIND><<<grid, 512, 0, s>>>(t);
-    return hipGetLastError();
-  } else {
+    if (KIND == GroupedKind::kDw || !t.few_rows) {
+      const uint32_t grid = static_cast<uint32_t>(tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256);   // of 256 CUs
+      grouped_stream_kernel<E, 128, 128, 2, 4, KIND><<<grid, 512, 0, s>>>(t);
+      return hipGetLastError();
+    }
+  }
+  if constexpr (KIND != GroupedKind::kDw) {
     return by_tiles(t, tiles, [&](const GroupedArgs& q, uint32_t n) {
       grouped_phased_kernel<E, 128, 128, 2, 4, KIND><<<n, 512, 0, s>>>(q);
     });
   }
+  return hipSuccess;
 }
 
 }  // namespace dsmoe

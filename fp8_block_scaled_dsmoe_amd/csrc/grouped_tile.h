@@ -26,6 +26,7 @@ struct GroupedArgs {
   uint32_t tiles_n;
   uint32_t run;            // consecutive tiles of an XCD
   uint64_t tile0;          // first tile of the launch
+  bool few_rows;           // k256: most tiles have few rows (grouped_gemm.hip)
 };
 
 // Blocks are dispatched round-robin over the XCDs.  In a round of kXcds * run
@@ -322,8 +323,8 @@ hipError_t by_tiles(GroupedArgs t, uint64_t tiles, F f) {
   return hipSuccess;
 }
 
-// 256 x 256 tiles: blocks that stay (grouped_stream.h) for y and dW, a block for
-// each tile for the gated product, whose longer epilogue would not stay in the
+// 256 x 256 tiles: blocks that stay (grouped_stream.h) for dW, and for y of more than
+// few rows per group (grouped_gemm.hip), a block for each tile for the gated product, whose longer epilogue would not stay in the
 // instruction cache (one token 200 us instead of 134; 4096 tokens to 256 experts
 // 3.30 ms instead of 3.08), and for dx, where the two are equal in whole tiles.
 template <Elem E, GroupedKind KIND>

@@ -6,12 +6,13 @@ import ctypes
 
 import numpy as np
 
-SHAPES = ("256x256", "128x128", "64x64", "32x128")
+SHAPES = ("256x256", "128x128", "64x64", "32x128", "256x256 each")
 PRODUCTS = ("y", "dx", "dw", "gated", "int8", "int8 gated")   # N, K of linear; gated: I, H
 
 # (product, groups, rows, N, K): shape.  256 x 256 tiles of y and dw by blocks that
 # stay: one tile a block, several of one chunk, of two and of many, wide and ragged.
-# Those of dx and gated have last tiles of every height.
+# Those of dx and gated, and of y by a block for each ("each"), have last tiles of
+# every height.
 SIZES = {
     ("y", 1, 5, 72, 72): "32x128",
     ("y", 7, 900, 1000, 201): "32x128",
@@ -22,6 +23,7 @@ SIZES = {
     ("y", 40, 12000, 520, 520): "256x256",
     ("y", 20, 9000, 1033, 1100): "256x256",
     ("y", 1, 9000, 4100, 1100): "256x256",
+    ("y", 40, 5120, 1033, 520): "256x256 each",
     ("dx", 1, 3, 72, 72): "32x128",
     ("dx", 3, 65, 520, 72): "64x64",
     ("dx", 300, 12000, 72, 72): "128x128",
@@ -43,6 +45,7 @@ SIZES = {
     ("int8", 300, 12000, 72, 72): "128x128",
     ("int8", 130, 39000, 136, 200): "256x256",
     ("int8", 20, 9000, 1033, 2100): "256x256",
+    ("int8", 40, 5120, 1033, 520): "256x256 each",
     ("int8 gated", 1, 5, 72, 72): "32x128",
     ("int8 gated", 40, 5200, 136, 72): "64x64",
     ("int8 gated", 130, 9100, 72, 72): "128x128",
