@@ -324,9 +324,10 @@ hipError_t by_tiles(GroupedArgs t, uint64_t tiles, F f) {
 }
 
 // 256 x 256 tiles: blocks that stay (grouped_stream.h) for dW, and for y of more than
-// few rows per group (grouped_gemm.hip), a block for each tile for the gated product, whose longer epilogue would not stay in the
-// instruction cache (one token 200 us instead of 134; 4096 tokens to 256 experts
-// 3.30 ms instead of 3.08), and for dx, where the two are equal in whole tiles.
+// few rows per group (grouped_gemm.hip); a block for each tile for the gated product,
+// whose longer epilogue would not stay in the instruction cache (one token 200 us
+// instead of 134; 4096 tokens to 256 experts, in whole tiles, 3.30 ms instead of
+// 3.08), and for dx, where the two are equal in whole tiles.
 template <Elem E, GroupedKind KIND>
 hipError_t launch_grouped_256(const GroupedArgs& t, uint64_t tiles, hipStream_t s);
 
