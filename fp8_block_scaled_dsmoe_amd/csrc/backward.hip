@@ -20,6 +20,7 @@
 //    selects and gets no gradient).
 #include "common.h"
 #include "kernels.h"
+#include "router_grad.h"
 
 namespace dsmoe {
 namespace {
@@ -436,11 +437,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const float* __restrict
 // ---------------------------------------------------------------------------
 // gate_grad_kernel: one block per token.  dgate[t][k] = <dy[t], o[inv[t][k]]>
 // (float32 products summed per thread over 8-column runs, then over the
-// block in a fixed order); then, as in the forward's routing, s = fl32(1 / (1
-// + e^-z)) evaluated in double, sum = float32 sum of the chosen s in
-// selection order, gate_k = s_k / sum, and
-// dlogits[t][e_k] = s_k (1 - s_k) (dgate_k - sum_j dgate_j gate_j) / sum; the
-// other logits get 0.
+// block in a fixed order); then dlogits[t][e_k] = s_k (1 - s_k) (dgate_k - sum_j
+// dgate_j gate_j) / sum by the first wave (router_grad.h); the other logits get 0.
 // ---------------------------------------------------------------------------
 template <bool kOF32>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ o,
@@ -450,7 +448,6 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
                                                         int64_t H, float* __restrict__ dgate,
                                                         float* __restrict__ dlogits) {
   __shared__ float s_part[4][32];
-  __shared__ float s_dg[32];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int k = 0; k < K; ++k) {
@@ -488,23 +485,16 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
     if (lane == 0) s_part[wave][k] = sum;
   }
   __syncthreads();
-  if (tid < K) s_dg[tid] = ((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid];
   for (int e = tid; e < E; e += 256) dlogits[t * E + e] = 0.f;
   __syncthreads();
-  if (tid == 0) {
-    float s[32];
-    float tot = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const double zd = static_cast<double>(logits[t * E + topk[t * K + k]]);
-      s[k] = static_cast<float>(1.0 / (1.0 + exp(-zd)));
-      tot = k == 0 ? s[k] : tot + s[k];
-    }
-    float mix = 0.f;
-    for (int k = 0; k < K; ++k) mix = __builtin_fmaf(s_dg[k], s[k] / tot, mix);
-    for (int k = 0; k < K; ++k) {
-      dgate[t * K + k] = s_dg[k];
-      const float ds = (s_dg[k] - mix) / tot;
-      dlogits[t * E + topk[t * K + k]] = ds * s[k] * (1.0f - s[k]);
+  if (wave == 0) {
+    const bool in = lane < K;
+    const int32_t e = in ? topk[t * K + lane] : 0;
+    const float dg = in ? ((s_part[0][lane] + s_part[1][lane]) + s_part[2][lane]) + s_part[3][lane] : 0.f;
+    const float v = router_logit_grad(in ? logits[t * E + e] : 0.f, dg, in, K);
+    if (in) {
+      dgate[t * K + lane] = dg;
+      dlogits[t * E + e] = v;
     }
   }
 }

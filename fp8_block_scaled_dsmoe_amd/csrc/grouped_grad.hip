@@ -6,6 +6,7 @@
 #include "act.h"
 #include "common.h"
 #include "grouped.h"
+#include "router_grad.h"
 #include "vec8.h"
 
 namespace dsmoe {
@@ -88,12 +89,7 @@ __global__ __launch_bounds__(256) void router_grad_kernel(const float* __restric
     // lane k < K holds the k-th choice
     const int32_t e = lane < K ? topk[t * K + lane] : -1;
     const bool in = e >= 0 && e < E;
-    const float s = in ? static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logits[t * E + e])))) : 0.0f;
-    const float d = in ? dgate[t * K + lane] : 0.0f;
-    float total = 0.0f, mix = 0.0f;
-    for (int k = 0; k < K; ++k) total += __shfl(s, k, 64);
-    for (int k = 0; k < K; ++k) mix = __builtin_fmaf(__shfl(d, k, 64), __shfl(s, k, 64) / total, mix);
-    const float v = (d - mix) / total * s * (1.0f - s);
+    const float v = router_logit_grad(in ? logits[t * E + e] : 0.0f, in ? dgate[t * K + lane] : 0.0f, in, K);
     for (int32_t c0 = 0; c0 < E; c0 += 64) {
       const int32_t c = c0 + lane;
       float o = 0.0f;

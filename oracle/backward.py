@@ -28,7 +28,6 @@ import numpy as np
 from .e4m3 import decode
 from .gemm import grouped_gemm
 from .quant import quant_act_1x128
-from .route import affinity
 
 
 def transpose_blocks(q: np.ndarray, s: np.ndarray):
@@ -69,8 +68,9 @@ __all__ = ["transpose_blocks", "dgrad_grouped"]
 # expert.  gate_k = s_k / sum_j s_j over the chosen experts and s = sigmoid(z)
 # (the readings of the forward), so the router logits receive
 # dz_e = s_e (1 - s_e) (dgate_e - sum_j dgate_j gate_j) / sum_j s_j for the
-# chosen experts and nothing for the others; the bias b, used only to select,
-# receives no gradient (it is moved by the balancing rule instead).
+# chosen experts and nothing for the others (1 - s_e as sigmoid(-z_e), which keeps
+# its digits where s_e is near 1); the bias b, used only to select, receives no
+# gradient (it is moved by the balancing rule instead).
 
 
 def chunk_offsets(offsets) -> np.ndarray:
@@ -163,14 +163,16 @@ def gate_backward(dy, o, topk_idx, logits, n_experts):
     """
     dy = np.asarray(dy, np.float64)
     o = np.asarray(o, np.float64)
-    s = affinity(logits).astype(np.float64)
-    s_sel = np.take_along_axis(s, np.asarray(topk_idx, np.int64), axis=1)
-    tot = s_sel.sum(axis=1, keepdims=True)
-    gates = s_sel / tot
+    idx = np.asarray(topk_idx, np.int64)
+    z = np.take_along_axis(np.asarray(logits, np.float32).astype(np.float64), idx, axis=1)
+    with np.errstate(over="ignore"):
+        s, q = 1.0 / (1.0 + np.exp(-z)), 1.0 / (1.0 + np.exp(z))      # q = 1 - s, with its digits
+    gates = s / s.sum(axis=1, keepdims=True)
     dgate = np.einsum("th,tkh->tk", dy, o)
-    ds = (dgate - np.sum(dgate * gates, axis=1, keepdims=True)) / tot
+    # dgate_k - sum_j dgate_j gate_j, the gates' sum being 1
+    apart = np.einsum("tkj,tj->tk", dgate[:, :, None] - dgate[:, None, :], gates)
     dz = np.zeros((dy.shape[0], n_experts))
-    np.put_along_axis(dz, np.asarray(topk_idx, np.int64), ds * s_sel * (1.0 - s_sel), axis=1)
+    np.put_along_axis(dz, idx, apart * gates * q, axis=1)
     return dgate, dz
 
 

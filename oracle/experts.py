@@ -107,10 +107,12 @@ def router_backward(dgate, topk, logits):
     dgate, logits = _f64(dgate), _f64(logits)
     out = np.zeros(logits.shape)
     for t in range(logits.shape[0]):
-        s = 1.0 / (1.0 + np.exp(-logits[t, topk[t]]))
-        total = s.sum()
-        mix = (dgate[t] * s).sum() / total
-        out[t, topk[t]] = (dgate[t] - mix) / total * s * (1.0 - s)
+        z = logits[t, topk[t]]
+        gate = 1.0 / (1.0 + np.exp(-z))
+        gate /= gate.sum()
+        # dgate_k - sum_j dgate_j gate_j, and 1 - s, without cancellation
+        apart = (dgate[t][:, None] - dgate[t][None, :]) @ gate
+        out[t, topk[t]] = apart * gate / (1.0 + np.exp(z))
     return out
 
 
