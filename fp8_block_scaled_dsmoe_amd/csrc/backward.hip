@@ -448,6 +448,8 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
                                                         int64_t H, float* __restrict__ dgate,
                                                         float* __restrict__ dlogits) {
   __shared__ float s_part[4][32];
+  __shared__ int32_t s_top[32];
+  __shared__ float s_dz[32];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int k = 0; k < K; ++k) {
@@ -485,8 +487,6 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
     if (lane == 0) s_part[wave][k] = sum;
   }
   __syncthreads();
-  for (int e = tid; e < E; e += 256) dlogits[t * E + e] = 0.f;
-  __syncthreads();
   if (wave == 0) {
     const bool in = lane < K;
     const int32_t e = in ? topk[t * K + lane] : 0;
@@ -494,8 +494,16 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t* __restri
     const float v = router_logit_grad(in ? logits[t * E + e] : 0.f, dg, in, K);
     if (in) {
       dgate[t * K + lane] = dg;
-      dlogits[t * E + e] = v;
+      s_top[lane] = e;
+      s_dz[lane] = v;
     }
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += 256) {
+    float v = 0.f;
+    for (int k = 0; k < K; ++k)
+      if (s_top[k] == e) v += s_dz[k];   // an expert chosen twice has both
+    dlogits[t * E + e] = v;
   }
 }
 

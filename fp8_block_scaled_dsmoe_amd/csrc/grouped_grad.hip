@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void grouped_gated_grad_kernel(GroupedGatedGra
   }
 }
 
-// A wave per token: the row of dlogits cleared, then the chosen experts' values.
+// A wave per token: the chosen experts' values by lane, then the row of dlogits.
 // Bound by the launch (256 experts: 1 KB a token).
 __global__ __launch_bounds__(256) void router_grad_kernel(const float* __restrict__ dgate,
                                                           const int32_t* __restrict__ topk,
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256) void router_grad_kernel(const float* __restric
       for (int k = 0; k < K; ++k) {
         const int32_t ek = __shfl(e, k, 64);
         const float vk = __shfl(v, k, 64);
-        if (ek == c) o = vk;
+        if (ek == c) o += vk;   // an expert chosen twice has both
       }
       if (c < E) dlogits[t * E + c] = o;
     }

@@ -529,7 +529,7 @@ dsmoe_status dsmoe_swiglu_backward(const float* h, const float* da, const float*
  *   dlogits   [T][E] f32 (output): with s = sigmoid(z), S = sum of the chosen
  *             s, gate = s / S: s_k (1 - s_k) (dgate_k - sum_j dgate_j gate_j) / S
  *             at the chosen experts, 0 elsewhere (routing held fixed); evaluated
- *             in double and rounded once
+ *             in double and rounded once (an expert chosen twice gets the sum)
  * Requires H % 8 == 0, 1 <= K <= DSMOE_MAX_TOPK, K <= E <= DSMOE_MAX_EXPERTS.
  */
 dsmoe_status dsmoe_gate_backward(const void* dy, const void* o, int ot, const int32_t* inv,

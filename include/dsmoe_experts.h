@@ -131,7 +131,7 @@ dsmoe_status dsmoe_grouped_gated_linear_backward(const void* da, int64_t ldda, c
  *   dlogits   [T][E] f32 (output): with s = sigmoid(z), S = sum of the chosen
  *             s, gate = s / S: s_k (1 - s_k) (dgate_k - sum_j dgate_j gate_j) / S
  *             at the chosen experts, 0 elsewhere (routing held fixed); evaluated
- *             in double and rounded once
+ *             in double and rounded once (an expert chosen twice gets the sum)
  * An index outside [0, E) is left out.  Requires 1 <= K <= DSMOE_MAX_TOPK,
  * K <= E <= DSMOE_MAX_EXPERTS, T in [0, 2^31).
  */

@@ -172,7 +172,7 @@ def gate_backward(dy, o, topk_idx, logits, n_experts):
     # dgate_k - sum_j dgate_j gate_j, the gates' sum being 1
     apart = np.einsum("tkj,tj->tk", dgate[:, :, None] - dgate[:, None, :], gates)
     dz = np.zeros((dy.shape[0], n_experts))
-    np.put_along_axis(dz, idx, apart * gates * q, axis=1)
+    np.add.at(dz, (np.arange(dy.shape[0])[:, None], idx), apart * gates * q)   # an expert chosen twice: both
     return dgate, dz
 
 

@@ -112,7 +112,7 @@ def router_backward(dgate, topk, logits):
         gate /= gate.sum()
         # dgate_k - sum_j dgate_j gate_j, and 1 - s, without cancellation
         apart = (dgate[t][:, None] - dgate[t][None, :]) @ gate
-        out[t, topk[t]] = apart * gate / (1.0 + np.exp(z))
+        np.add.at(out[t], topk[t], apart * gate / (1.0 + np.exp(z)))   # an expert chosen twice: both
     return out
 
 

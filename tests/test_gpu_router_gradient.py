@@ -75,3 +75,30 @@ def test_gate_backward_keeps_its_digits(d, T, E, K, H, lo, hi, signs):
     assert np.abs(dg - want).max() <= 1e-5 * H
     _close(dz, oe.router_backward(dg, top, z), _bound(dg, top, z), "f32", "dlogits")
     assert np.allclose(want_z, oe.router_backward(want, top, z), rtol=1e-6, atol=0)
+
+
+def test_an_expert_chosen_twice_and_indices_outside(d):
+    """The gradients of an expert's choices add up, in either call; dsmoe_router_backward leaves indices outside [0, E)
+    out."""
+    banner("router gradient, an expert chosen twice")
+    r = np.random.default_rng(5)
+    T, E, K, H = 20, 70, 6, 64
+    z = r.standard_normal((T, E)).astype(np.float32)
+    top = np.stack([r.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    top[:, 3], top[::2, 5] = top[:, 0], top[::2, 0]
+    dg = r.standard_normal((T, K)).astype(np.float32)
+    # three roundings to float32 and two sums of them at most
+    size = np.zeros((T, E))
+    np.add.at(size, (np.arange(T)[:, None], top), np.abs(dg).max(1, keepdims=True) * 2.0 ** -22)
+    _close(d.router_backward(dev(dg), dev(top), dev(z)), oe.router_backward(dg, top, z), size, "f32", "router_backward")
+    inv = r.permutation(T * K).astype(np.int32).reshape(T, K)
+    dy, o = (dev(r.standard_normal(s).astype(np.float32), torch.bfloat16) for s in ((T, H), (T * K, H)))
+    dgate, dz = d.gate_backward(dy, o, dev(inv), dev(top), dev(z))
+    dg2 = host(dgate).astype(np.float64)
+    size2 = size / np.abs(dg).max(1, keepdims=True) * np.abs(dg2).max(1, keepdims=True)
+    _close(dz, oe.router_backward(dg2, top, z), size2, "f32", "gate_backward")
+    out = top.copy()
+    out[:, 0], out[:, 2] = -1, E
+    left = [1, 3, 4, 5]
+    _close(d.router_backward(dev(dg), dev(out), dev(z)), oe.router_backward(dg[:, left], out[:, left], z), size, "f32",
+           "indices outside")

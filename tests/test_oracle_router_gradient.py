@@ -32,3 +32,18 @@ def test_two_logits_far_apart():
     want = g[0, 0] * g[0, 1] * q * [1, -1]
     got = oe.router_backward(np.array([[1.0, 0.0]]), np.array([[0, 1]]), z)
     assert np.allclose(got, want, rtol=1e-12, atol=0)
+
+
+def test_an_expert_chosen_twice():
+    """Its logit moves both of its gates: the gradient is the sum, as differences give it."""
+    z, d = np.array([[0.3, -1.2, 2.0]]), np.array([[0.7, -0.4, 1.1]])
+    top = np.array([[2, 0, 2]])
+
+    def loss(z):
+        s = 1 / (1 + np.exp(-z[0, top[0]]))
+        return float((d[0] * s / s.sum()).sum())
+
+    num = [(loss(z + e) - loss(z - e)) / 2e-6 for e in 1e-6 * np.eye(3)]
+    assert np.allclose(oe.router_backward(d, top, z)[0], num, atol=1e-8)
+    _, dz = ob.gate_backward(np.ones((1, 1)), d[:, :, None], top, z, 3)    # z in float32 there
+    assert np.allclose(dz[0], num, atol=1e-6)
