@@ -45,8 +45,9 @@ struct GroupedGemm {
   const float* row_scale;    // [R] or null; kGated
   const float* a_scale;      // i8: [a.n]
   const float* w_scale;      // i8: [groups][N] (kGated: [2N])
-  // y (float32) += the result; kDx, kDw.  The call before had the same operands but
-  // for a's values, and a needs no copy: the other operand's is in the workspace.
+  // y (float32) += the result where y is finite (plus_rest); kDx, kDw.  The call
+  // before had the same operands but for a's values, and a needs no copy: the other
+  // operand's is in the workspace.
   bool add;
   void* y;
   int64_t ldy;

@@ -360,7 +360,7 @@ struct Stream : StreamCore<E, HM, HN, WM, WN, KIND> {
                   const int32_t at = hb * W + 16 * j + 4 * (lane >> 4);
                   load4(reinterpret_cast<const float*>(y + (r + (lane & 15)) * ld) + at, left - at, add);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) v[j][e] += add[e];
+                  for (int e = 0; e < 4; ++e) v[j][e] = plus_rest(add[e], v[j][e]);
                 }
               }
             }

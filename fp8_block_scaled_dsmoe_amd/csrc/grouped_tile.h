@@ -253,7 +253,7 @@ struct GroupedTile : TileCore<E, HM, HN, WM, WN, KIND == GroupedKind::kDw,
           float o[8];
           load8(p.y, y, true, left, o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += o[e];
+          for (int e = 0; e < 8; ++e) v[e] = plus_rest(o[e], v[e]);
         }
         store8(p.y, y, p.y_f32, left, v);
       }

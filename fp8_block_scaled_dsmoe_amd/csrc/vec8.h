@@ -112,6 +112,14 @@ __device__ __forceinline__ void rest8(float* v, const u32x4& q) {
   for (int e = 0; e < 8; ++e) v[e] = __builtin_isfinite(r[e]) ? v[e] - r[e] : 0.0f;
 }
 
+// The sum of the products of the two values that rest8 makes of one: where the
+// first's is infinite or NaN (the other operand is) it is the result, as the whole
+// value's product would be; the rest's is then infinite with any sign, or 0 times
+// infinity.
+__device__ __forceinline__ float plus_rest(float first, float rest) {
+  return __builtin_isfinite(first) ? first + rest : first;
+}
+
 // The same for values i, i + 1, ... of a matrix or vector whose type is known
 // at run time.
 __device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, int64_t left, float* o) {
