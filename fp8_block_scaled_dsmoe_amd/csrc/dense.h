@@ -81,6 +81,8 @@ struct DenseGemm {
   bool bias_f32;
   const void* residual;   // [M][N], type of y, or null
   int64_t ldr;
+  // the residual is the product of a's other part (vec8.h, plus_rest); no act, z or bias
+  bool rest;
   void* y;                // [M][N]
   int64_t ldy;
   bool y_f32;

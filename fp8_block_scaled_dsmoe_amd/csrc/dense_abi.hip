@@ -124,7 +124,7 @@ dsmoe_status run_products(const void* dz, const void* dz_lo, int64_t lddz, bool 
     const hipError_t e = dsmoe::launch_dense_gemm(g, st);
     if (e != hipSuccess || yt != DSMOE_F32 || !dz_lo) return e;
     g.a.p = static_cast<const uint16_t*>(dz_lo);
-    g.residual = y, g.ldr = ldy;
+    g.residual = y, g.ldr = ldy, g.rest = true;
     return dsmoe::launch_dense_gemm(g, st);
   };
   hipError_t e = hipSuccess;

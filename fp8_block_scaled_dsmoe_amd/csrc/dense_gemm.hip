@@ -52,7 +52,10 @@ __device__ __forceinline__ void finish_linear(const DenseGemm& p, int64_t m, int
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = act_f32(p.act, v[e]);
   }
-  if (p.residual) {
+  if (p.rest) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = plus_rest(r[e], v[e]);
+  } else if (p.residual) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
@@ -135,7 +138,7 @@ struct Tile : TileCore<Elem::kBf16, HM, HN, WM, WN, AT, BT, EPI == DenseEpi::kGa
   // a thread's rows is on its way before the results are in LDS (bf16: of both
   // halves; a batch of four rows at a time between the stores cost 4096 x 7168
   // x 2048 with a residual 27 us over the same without).
-  template <bool F32>
+  template <bool F32, bool REST>
   __device__ __forceinline__ void finish_plain(const Acc& acc) const {
     constexpr int R = HM / kRowsAtOnce, ES = F32 ? 4 : 2;
     const int run = threadIdx.x % kRuns, r0 = threadIdx.x / kRuns;
@@ -168,7 +171,7 @@ struct Tile : TileCore<Elem::kBf16, HM, HN, WM, WN, AT, BT, EPI == DenseEpi::kGa
         get(r, run * 8, v);
         unpack8<F32>(res[ha][q], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] + bias[e] + x[e];
+        for (int e = 0; e < 8; ++e) v[e] = REST ? plus_rest(x[e], v[e]) : v[e] + bias[e] + x[e];
         store8(p.y, m * p.ldy + n, F32, p.N - n, v);
       }
     }
@@ -177,10 +180,12 @@ struct Tile : TileCore<Elem::kBf16, HM, HN, WM, WN, AT, BT, EPI == DenseEpi::kGa
   __device__ __forceinline__ void finish(const Acc& acc) const {
     if constexpr (!kGated) {
       if (t.plain) {
-        if (p.y_f32)
-          finish_plain<true>(acc);
+        if (!p.y_f32)
+          finish_plain<false, false>(acc);
+        else if (p.rest)
+          finish_plain<true, true>(acc);
         else
-          finish_plain<false>(acc);
+          finish_plain<true, false>(acc);
         return;
       }
     }

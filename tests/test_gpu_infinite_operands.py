@@ -6,8 +6,10 @@ import pytest
 import torch
 
 from gpu_util import banner
+from oracle import dense as od
 from oracle import experts as oe
 from test_gpu_dense import V, _mat
+from test_gpu_dense import _grad_check as _dense_check
 from test_gpu_experts import _experts, _grad_check, _offsets
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +54,29 @@ def test_grouped_gated_linear_backward(d, sizes, I, H):
     bound = 4 * V * V + 2.0 ** -19
     _grad_check(dx, None, dz, x64, wx, off, bound, "f32", None, "dx elsewhere")
     _grad_check(None, dw, dz, ww, w64, off, bound, None, "f32", "dw elsewhere")
+
+
+# few rows (split contraction), 64 x 64 to 256 x 256 tiles
+@pytest.mark.parametrize("M,N,K", [(40, 72, 136), (300, 264, 136), (2048, 1024, 1033), (4096, 2048, 2048)])
+def test_dense_backward(d, M, N, K):
+    banner(f"dense, infinite x and w: {M} {N} {K}")
+    r = np.random.default_rng(M)
+    x, x64 = _mat(r, M, K)
+    w, w64 = _mat(r, N, K, 0.1)
+    dy, dy64 = _mat(r, M, N, 0.1)
+    z, z64 = _mat(r, M, N, 1.5)
+    h, h64 = _mat(r, M, N, 1.5)
+    da, da64 = _mat(r, M, N // 2, 0.1)
+    forms = {"linear": od.linear_backward(dy64, x64, w64, z64, "silu")[3], "gated": od.gated_linear_backward(da64, x64, w64, h64, "silu")[2]}
+    x[5, 7] = float("inf")
+    w[3, 11] = -float("inf")
+    x64[:, 7], w64[:, 11] = 0, 0
+    for form, dz in forms.items():
+        if form == "linear":
+            dx, dw, _ = d.linear_backward(dy, x, w, z, "silu", F32, F32)
+        else:
+            dx, dw = d.gated_linear_backward(da, x, w, h, "silu", F32, F32)
+        _signs(dw[:, 7], dz[5], form + " dw")
+        _signs(dx[:, 11], -dz[:, 3], form + " dx")
+        dx[:, 11], dw[:, 7] = 0, 0
+        _dense_check(dx, dw, None, (dz @ w64, dz.T @ x64, None, dz), None, x64, w64, True, "f32", "f32", form)
