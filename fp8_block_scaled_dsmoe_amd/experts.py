@@ -384,7 +384,7 @@ def _routed_rows(routing, n_shared):
 
 
 def moe_ffn_forward(x: torch.Tensor, routing: dict, w13: torch.Tensor, w2: torch.Tensor, act: str = "silu",
-                    n_shared: int = 0, training: bool = False):
+                    n_shared: int = 0, training: bool = False, out_dtype=torch.bfloat16):
     """The experts' feed-forward pass in bf16:
 
         y[t] = sum over the experts e of token t of
@@ -392,43 +392,49 @@ def moe_ffn_forward(x: torch.Tensor, routing: dict, w13: torch.Tensor, w2: torch
 
     x bf16 [T][H], routing as from route(); w13 bf16 [E][2I][H], w2 bf16
     [E][H][I], with n_shared = 1 one more expert that every token takes with
-    gate 1.  H is a multiple of 8.  Returns (y, saved): y bf16 [T][H] and, when
-    training, what moe_ffn_backward needs."""
+    gate 1.  H is a multiple of 8, E + n_shared at most 1024.  out_dtype is the
+    type of y and of the terms that the sum over the experts adds up in float32:
+    in bf16 each is rounded on the way, as y is at the end, which saves half of
+    their bytes; float32 (as the FP8 layer's) rounds neither.  Returns (y, saved):
+    y [T][H] and, when training, what moe_ffn_backward needs."""
     off, perm, scale, shared0 = _routed_rows(routing, n_shared)
     _tokens(x, routing)
     a, h = grouped_gated_linear(x, w13, off, act, rows=perm, row_scale=scale, save_h=training)
-    o = grouped_linear(a, w2, off)
+    o = grouped_linear(a, w2, off, out_dtype=out_dtype)
     y = combine_rows(o, routing["inv"], shared0)
     return y, ({"offsets": off, "perm": perm, "scale": scale, "shared0": shared0, "a": a, "h": h} if training else None)
 
 
 def moe_ffn_backward(dy: torch.Tensor, x: torch.Tensor, routing: dict, w13: torch.Tensor, w2: torch.Tensor,
                      saved: dict, act: str = "silu", logits: Optional[torch.Tensor] = None, dw_dtype=torch.float32,
-                     dz_dtype: Optional[torch.dtype] = None):
+                     dz_dtype: Optional[torch.dtype] = None, dx_dtype=torch.bfloat16):
     """Gradients of moe_ffn_forward from dy bf16 [T][H] and its saved dict;
-    dz_dtype as in grouped_gated_linear_backward.  Returns {"dx" bf16 [T][H],
-    "dw13", "dw2", "dgates" f32 [T][K]} and, with the router logits f32 [T][E],
-    "dlogits" (the routing held fixed)."""
+    dz_dtype as in grouped_gated_linear_backward; dx_dtype the type of dx and of
+    the terms that its sum over a token's experts adds up, as out_dtype of the
+    forward.  The gradient at the activations is bf16, as the operand of what
+    follows.  Returns {"dx" [T][H], "dw13", "dw2", "dgates" f32 [T][K]} and, with
+    the router logits f32 [T][E], "dlogits" (the routing held fixed)."""
     off, perm, inv = saved["offsets"], saved["perm"], routing["inv"]
     if dy.shape != x.shape or x.shape[0] != inv.shape[0]:
         raise ValueError("dy and x must be [T][H] with the routing's T")
     da, dw2 = grouped_linear_backward(dy, saved["a"], w2, off, dy_rows=perm, dw_dtype=dw_dtype)
     dx_rows, dw13, dscale = grouped_gated_linear_backward(da, x, w13, saved["h"], off, act, rows=perm,
-                                                          row_scale=saved["scale"], dw_dtype=dw_dtype,
-                                                          need_dscale=True, dz_dtype=dz_dtype)
+                                                          row_scale=saved["scale"], dx_dtype=dx_dtype,
+                                                          dw_dtype=dw_dtype, need_dscale=True, dz_dtype=dz_dtype)
     out = {"dx": combine_rows(dx_rows, inv, saved["shared0"]), "dw13": dw13, "dw2": dw2, "dgates": dscale[inv.long()]}
     if logits is not None:
         out["dlogits"] = router_backward(out["dgates"], routing["topk_idx"], logits)
     return out
 
 
-def moe_ffn_int8_forward(x: torch.Tensor, routing: dict, w13: tuple, w2: tuple, act: str = "silu", n_shared: int = 0):
+def moe_ffn_int8_forward(x: torch.Tensor, routing: dict, w13: tuple, w2: tuple, act: str = "silu", n_shared: int = 0,
+                         out_dtype=torch.bfloat16):
     """moe_ffn_forward on 8-bit integers: w13 and w2 are (codes, scales) of the
     experts' weights as from quant_rows_int8; x and the activations are
-    quantised per row on the way.  x bf16 [T][H]; returns y bf16 [T][H]."""
+    quantised per row on the way.  x bf16 [T][H]; returns y [T][H]."""
     off, perm, scale, shared0 = _routed_rows(routing, n_shared)
     _tokens(x, routing)
     q, s = quant_rows_int8(x)
     a = int8_gated_linear(q, s, *w13, off, act, rows=perm, row_scale=scale)
     q, s = quant_rows_int8(a)
-    return combine_rows(int8_linear(q, s, *w2, off), routing["inv"], shared0)
+    return combine_rows(int8_linear(q, s, *w2, off, out_dtype=out_dtype), routing["inv"], shared0)
