@@ -6,6 +6,7 @@
 #include "dense.h"
 #include "dsmoe_experts.h"
 #include "grouped.h"
+#include "grouped_walk.h"
 #include "host.h"
 
 namespace {
@@ -185,6 +186,49 @@ int dsmoe_grouped_shape(int product, int32_t G, int64_t R, int64_t N, int64_t K)
     default: return dsmoe::grouped_gemm_shape(row_product(GroupedKind::kGated, product == 5, a, nullptr, ld, g, N, K));
   }
 }
+
+// Not part of the interface: the tiles that block `block` of `blocks` blocks that stay
+// takes, in their order, for y [R][N] (dw 0) or dw [N][K] of bf16 operands, from
+// offsets in host memory (NULL: one group): group, m0, m_end, n0, k0, k1 and chunks of
+// the first `most`.  Returns their number, or -1.
+int64_t dsmoe_grouped_walk(int dw, const int32_t* offsets, int32_t G, int64_t R, int64_t N, int64_t K, uint32_t block,
+                           uint32_t blocks, int32_t* out, int64_t most) {
+  constexpr int kRows = 256, kCols = 256, kChunk = 64;
+  constexpr uint32_t kXcds = 8;
+  if (!groups_ok(G) || !rows_ok(R) || !dim_ok(N) || !dim_ok(K) || !fits(G, R, N, K) || (!offsets && G != 1) ||
+      blocks == 0 || blocks % kXcds != 0 || block >= blocks)
+    return -1;
+  int32_t begin[DSMOE_MAX_EXPERTS], end[DSMOE_MAX_EXPERTS], first[DSMOE_MAX_EXPERTS + 1];
+  auto clamped = [&](int32_t v) { return v < 0 ? 0 : v > R ? static_cast<int32_t>(R) : v; };
+  uint32_t before = 0;
+  for (int32_t g = 0; g < G; ++g) {
+    begin[g] = offsets ? clamped(offsets[g]) : 0;
+    end[g] = offsets ? clamped(offsets[g + 1]) : static_cast<int32_t>(R);
+    if (end[g] < begin[g]) end[g] = begin[g];
+    first[g] = static_cast<int32_t>(before);
+    before += (static_cast<uint32_t>(end[g] - begin[g]) + kRows - 1) / kRows;
+  }
+  first[G] = static_cast<int32_t>(before);
+  const int64_t cols = dw ? K : N;
+  const dsmoe::StreamSizes s{G, static_cast<int32_t>(N), static_cast<int32_t>((K + kChunk - 1) / kChunk),
+                             static_cast<uint32_t>((N + kRows - 1) / kRows), static_cast<uint32_t>((cols + kCols - 1) / kCols)};
+  auto read = [](const int32_t& v) { return v; };
+  uint32_t tile = dsmoe::first_stream_tile(block, blocks, kXcds);
+  int32_t walk = 0;
+  dsmoe::StreamTile d{};
+  int64_t n = 0;
+  while (dw ? dsmoe::next_stream_tile<true, kRows, kCols, kChunk>(s, begin, end, first, blocks, tile, walk, read, d)
+            : dsmoe::next_stream_tile<false, kRows, kCols, kChunk>(s, begin, end, first, blocks, tile, walk, read, d)) {
+    const int32_t v[7] = {d.group, d.m0, d.m_end, d.n0, d.k0, d.k1, d.chunks};
+    if (n < most)
+      for (int i = 0; i < 7; ++i) out[7 * n + i] = v[i];
+    ++n;
+  }
+  return n;
+}
+// Not part of the interface: the tiles that the copies may have entered past the
+// products' tile, which the queue of those blocks is sized by.
+int dsmoe_grouped_walk_ahead(void) { return dsmoe::kStreamAhead; }
 
 size_t dsmoe_grouped_linear_workspace_bytes(const void* x, int64_t ldx, int64_t n, const int32_t* rows,
                                             const void* w, int64_t ldw, int32_t G, int64_t R, int64_t N, int64_t K) {

@@ -18,17 +18,9 @@
 
 #include "dsmoe.h"
 #include "grouped_tile.h"
+#include "grouped_walk.h"
 
 namespace dsmoe {
-
-// What of the problem a tile is: rows [m0, m_end) of the result at most (kDw: of
-// the group's), columns from n0 on.
-struct StreamTile {
-  int32_t group;
-  int32_t m0, m_end, n0;
-  int32_t k0, k1;        // kDw: the group's rows
-  int32_t chunks;        // at least 1: a group without rows has one of zeros
-};
 
 // The kernel's arguments, read again: what is read through it does not stay in
 // scalar registers over the loop.
@@ -62,7 +54,11 @@ struct Stream : StreamCore<E, HM, HN, WM, WN, KIND> {
   static constexpr int kCols = 2 * HN, W = HN / WN;   // of a tile; of a wave in either half
   static constexpr int kWide = 2 * W;                 // a wave's columns in the result, side by side
   static constexpr int kMaxGroups = DSMOE_MAX_EXPERTS;
-  static constexpr int kQueue = 4, kEntry = 8;   // tiles, integers of one
+  // The queue: tiles (a power of 2), integers of one.  It holds the products' tile,
+  // whose entry is free once the next one is popped, and those that the copies have
+  // entered past it.
+  static constexpr int kQueue = 4, kEntry = 8;
+  static_assert(kQueue >= 1 + kStreamAhead && (kQueue & (kQueue - 1)) == 0, "an entered tile's entry may not be in use");
 
   const GroupedArgs& t;
   const GroupedGemm& p;
@@ -70,8 +66,7 @@ struct Stream : StreamCore<E, HM, HN, WM, WN, KIND> {
   const Table& table;
   uint32_t tile;             // the copies' next
   int32_t walk;              // its group at least
-  // The tiles whose products are not done: the copies are up to two tiles ahead
-  // (of one chunk each).  A queue of the wave's own in LDS.
+  // The tiles whose products are not done: a queue of the wave's own in LDS.
   int32_t* const queue;
   int32_t entered, done;
   StreamTile pt;             // the products' tile
@@ -104,58 +99,17 @@ struct Stream : StreamCore<E, HM, HN, WM, WN, KIND> {
     if constexpr (!kDw)
       if (wave == 0 && lane == 0) s.first[p.groups.n] = before;
     __syncthreads();
-    // each XCD a run of consecutive tiles
-    tile = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    tile = first_stream_tile(blockIdx.x, gridDim.x, kXcds);
     walk = 0;
     entered = done = 0;
   }
 
   // The copies' next tile; false past the last.
   __device__ __forceinline__ bool next(StreamTile& d) {
-    constexpr uint32_t kBand = kDw ? 8 : 4;   // row tiles that share their columns' rows in L2
-    uint32_t local, rows;
-    if constexpr (kDw) {
-      const uint32_t per_group = t.tiles_m * t.tiles_n;
-      const uint32_t g = tile / per_group;
-      if (g >= static_cast<uint32_t>(p.groups.n)) return false;
-      d.group = static_cast<int32_t>(g);
-      local = tile - g * per_group;
-      rows = t.tiles_m;
-    } else {
-      // tile >= table.first[walk] * tiles_n
-      int32_t f0 = __builtin_amdgcn_readfirstlane(table.first[walk]), f1 = f0;
-      while (walk < p.groups.n) {
-        f1 = __builtin_amdgcn_readfirstlane(table.first[walk + 1]);
-        if (tile < static_cast<uint32_t>(f1) * t.tiles_n) break;
-        f0 = f1;
-        ++walk;
-      }
-      if (walk >= p.groups.n) return false;
-      d.group = walk;
-      local = tile - static_cast<uint32_t>(f0) * t.tiles_n;
-      rows = static_cast<uint32_t>(f1 - f0);
-    }
-    // past the group only where offsets that break the rule let a count wrap
-    if (local >= rows * t.tiles_n) return false;
-    const int32_t lo = __builtin_amdgcn_readfirstlane(table.begin[d.group]);
-    const int32_t hi = __builtin_amdgcn_readfirstlane(table.end[d.group]);
-    const uint32_t per_band = kBand * t.tiles_n, band = local / per_band, in = local - band * per_band;
-    const uint32_t high = min(kBand, rows - band * kBand);
-    const uint32_t tn = in / high, tm = band * kBand + (in - tn * high);
-    d.n0 = static_cast<int32_t>(tn) * kCols;
-    d.m0 = static_cast<int32_t>(tm) * 2 * HM;
-    if constexpr (kDw) {
-      d.m_end = static_cast<int32_t>(p.N);
-      d.k0 = lo, d.k1 = hi;
-      d.chunks = max(1, static_cast<int32_t>((static_cast<uint32_t>(hi - lo) + Core::kChunk - 1) / Core::kChunk));
-    } else {
-      d.m0 += lo;
-      d.m_end = hi;
-      d.k0 = d.k1 = 0;
-      d.chunks = t.chunks;
-    }
-    tile += gridDim.x;
-    return true;
+    const StreamSizes z{p.groups.n, static_cast<int32_t>(p.N), t.chunks, t.tiles_m, t.tiles_n};
+    return next_stream_tile<kDw, 2 * HM, kCols, Core::kChunk>(
+        z, table.begin, table.end, table.first, gridDim.x, tile, walk,
+        [](const int32_t& v) { return __builtin_amdgcn_readfirstlane(v); }, d);
   }
   // The products' tile: the queue's head.
   __device__ __forceinline__ void head() {
