@@ -122,19 +122,28 @@ constexpr ShapeInfo kShapes[] = {{256, 256, 1, 1.42, 1.42, 7.0, 4.0},
 // to 108 measured sizes (16 to 320 rows per expert, 16 and 64 experts, 1024 x 512 to
 // 7168 x 2048, bf16 and 8 bits): the shape taken is 1.0% from the best on average,
 // 20% at worst (16 rows of 2048 x 1024, 29 us); by whole tiles' times 3.9%, 52% at
-// worst.  64 experts of 7168 x 2048 with 48 rows, dx: 647 us, 128 x 128 677, 64 x 64
+// worst.  Where the groups are uneven, which the host does not know, more is lost:
+// with popularities falling as the rank's square root 3.8% on average over 315 sizes
+// (4 to 768 rows per expert, every product; even popularities 1.2% over the same), 5%
+// of the sizes lose more than 23%, and small products most (64 experts of 1024 -> 512
+// with 192 rows in 8 bits 51 us, in 128 x 128 tiles 32).  64 experts of 7168 x 2048 with 48 rows, dx: 647 us, 128 x 128 677, 64 x 64
 // 883; with 96 rows gated 653 us, 768, 1047.
-// y takes these blocks up to the last entry's rows, past it those that stay
-// (grouped_stream.h): 256 experts of 7168 x 2048 with 128 rows 1.67 ms, 1.73 by blocks
-// that stay, in 8 bits 0.91, 0.99; with 192 rows 1.83, 1.82 and 1.07, 1.07; with 224
-// 1.95, 1.87 and 1.15, 1.11; with 256 2.43, 2.36 and 1.47, 1.41.  64 of 1024 x 512 with
-// 192 rows 25 us, 31 and 22, 28; with 224 26, 31 and 23, 29; with 256 45, 45.
+// y takes these blocks up to 192 rows per group, and up to 224 where there are at most
+// kFewTiles tiles, so that the start of a tile's copies under the tile before matters
+// less; past that those that stay (grouped_stream.h).  Their time by that of blocks that
+// stay, on average over 7 sizes of 1024 x 512 to 2048 x 7168 with 8 to 256 experts, in
+// both types, and in brackets with more than kFewTiles tiles: 160 rows 0.91 (0.99), 192
+// 0.92 (1.00, at worst 1.09), 224 0.95 (1.03, at worst 1.14), 240 0.97 (1.03).  256
+// experts of 7168 x 2048 with 192 rows 1.82 ms, 1.80 by blocks that stay, in 8 bits 1.07,
+// 1.05; with 224 1.91, 1.85 and 1.13, 1.10.  64 of 1024 x 512 with 192 rows 24 us, 30
+// and 22, 29; with 224 38, 42 and 34, 38.
 struct ShortTile {
   double rows, chunk_us;
 };
 constexpr ShortTile kShort[] = {{128, 0.8}, {192, 1.1}, {224, 1.42}};
 constexpr double kShortEnd = 9.0;
 constexpr int64_t kCus = 256;
+constexpr double kFewTiles = 4.0 * kCus;
 constexpr double kRead = 6.1e6, kWrite = 4.0e6;   // bytes per us of weights, of their gradients
 
 // Time of `tiles` tiles of `chunks` chunks: rounds of the card.
@@ -177,7 +186,7 @@ GroupedPlan make_plan(const GroupedGemm& p) {
     } else {
       double tm = G == 1 ? static_cast<double>((R + s.rows - 1) / s.rows) : per_group / s.rows + 0.5;
       if (i == 0) {
-        q.few_rows = per_group <= kShort[2].rows;
+        q.few_rows = per_group <= kShort[busy * tn <= kFewTiles ? 2 : 1].rows;
         if (gated || dx || q.few_rows) s.end_us = kShortEnd;
         for (const ShortTile& t : kShort) {
           if (per_group > t.rows) continue;

@@ -141,3 +141,15 @@ def test_copies_ahead_of_the_products(lib):
         assert seen == [[(i, c)] * 4 for i, n in enumerate(chunks) for c in range(n)]
         worst = max(worst, ahead)
     assert worst == lib.dsmoe_grouped_walk_ahead()
+
+
+def test_when_blocks_stay(lib):
+    """y in 256 x 256 tiles: a block for each tile up to 192 rows per group, and up to 224 where there are at most four
+    tiles a CU, as measured; blocks that stay past that."""
+    import grouped_kernels as gk
+    for product in ("y", "int8"):
+        for G, N, K, rows in ((256, 7168, 2048, 192), (64, 7168, 2048, 160), (64, 1024, 512, 208), (32, 2048, 7168, 224)):
+            assert gk.shape(lib, product, G, G * rows, N, K) == "256x256 each", (G, N, K, rows)
+        for G, N, K, rows in ((256, 7168, 2048, 208), (256, 7168, 2048, 224), (64, 7168, 2048, 208), (256, 2048, 512, 224),
+                              (32, 4096, 4096, 320)):
+            assert gk.shape(lib, product, G, G * rows, N, K) == "256x256", (G, N, K, rows)
