@@ -89,17 +89,7 @@ __global__ __launch_bounds__(256) void router_grad_kernel(const float* __restric
     // lane k < K holds the k-th choice
     const int32_t e = lane < K ? topk[t * K + lane] : -1;
     const bool in = e >= 0 && e < E;
-    const float v = router_logit_grad(in ? logits[t * E + e] : 0.0f, in ? dgate[t * K + lane] : 0.0f, in, K);
-    for (int32_t c0 = 0; c0 < E; c0 += 64) {
-      const int32_t c = c0 + lane;
-      float o = 0.0f;
-      for (int k = 0; k < K; ++k) {
-        const int32_t ek = __shfl(e, k, 64);
-        const float vk = __shfl(v, k, 64);
-        if (ek == c) o += vk;   // an expert chosen twice has both
-      }
-      if (c < E) dlogits[t * E + c] = o;
-    }
+    write_router_grad(e, in ? logits[t * E + e] : 0.0f, in ? dgate[t * K + lane] : 0.0f, in, K, E, dlogits + t * E);
   }
 }
 
