@@ -9,11 +9,12 @@
 // Bound by the copies and LDS reads beside the matrix instructions, 1.42 us a chunk
 // (64 KB copied, 192 KB read from LDS by the waves; without the products 1.3), and
 // by the tile's border, 5 to 7 us of first chunks from memory, turning and storing
-// 128 KB of results.  A block for each tile, against these: y of 256 experts, 262144
-// rows of uneven groups, 7168 x 2048: 6.99 ms, 6.67; dW of 32 experts with 512 rows,
-// 7168 x 2048, float32: 920 us, 870; 8-bit 4096 x 7168 x 2048: 80 us, 76.  Writing in
-// two halves, each while the SIMD's other wave multiplies: dW 598 instead of 575 in
-// bf16.
+// 128 KB of results.  A block for each tile, against these, on one card: y of 256
+// experts, 262144 rows of uneven groups, 7168 x 2048 (grouped_phased_kernel): 7.13 ms,
+// 6.70; dW of 32 experts with 512 rows each, 7168 x 2048 (this kernel with as many blocks
+// as tiles): 671 us, 568 in bf16, 795, 755 in float32, in uneven groups 748, 585 and
+// 988, 778; 8-bit 4096 x 7168 x 2048: 70 us, 67.  Writing in two halves, each while the
+// SIMD's other wave multiplies: dW 598 instead of 575 in bf16.
 #pragma once
 
 #include "dsmoe.h"

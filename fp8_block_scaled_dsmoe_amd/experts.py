@@ -222,8 +222,10 @@ def grouped_gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w13: torch.
                                   dz_dtype: Optional[torch.dtype] = None):
     """Gradients of grouped_gated_linear (dsmoe_grouped_gated_linear_backward)
     from the saved h.  da bf16 [R][I].  Float32 gradients keep 16 bits of the
-    gradient at h, at twice a product's time; dz_dtype torch.bfloat16 rounds it
-    to bf16 for them too, as for bf16 gradients.  Returns (dx [R][H], one row per
+    gradient at h by a second product, which takes longer than the first, as it
+    reads the result back; dz_dtype torch.bfloat16 rounds it to bf16 for them too,
+    as for bf16 gradients, whose error is then 1.4 times their own rounding's (a
+    float32 gradient that is rounded afterwards has only that).  Returns (dx [R][H], one row per
     routed row, dw13 [G][2I][H], dscale f32 [R]), None where not wanted."""
     device, stream = _begin(da, "da")
     code = _grad_act(act, dz_dtype)
