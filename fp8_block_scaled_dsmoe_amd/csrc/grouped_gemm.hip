@@ -126,8 +126,9 @@ constexpr ShapeInfo kShapes[] = {{256, 256, 1, 1.42, 1.42, 7.0, 4.0},
 // with popularities falling as the rank's square root 3.8% on average over 315 sizes
 // (4 to 768 rows per expert, every product; even popularities 1.2% over the same), 5%
 // of the sizes lose more than 23%, and small products most (64 experts of 1024 -> 512
-// with 192 rows in 8 bits 51 us, in 128 x 128 tiles 32).  64 experts of 7168 x 2048 with 48 rows, dx: 647 us, 128 x 128 677, 64 x 64
-// 883; with 96 rows gated 653 us, 768, 1047.
+// with 192 rows in 8 bits 51 us, in 128 x 128 tiles 32).
+// 64 experts of 7168 x 2048 with 48 rows, dx: 647 us, 128 x 128 677, 64 x 64 883; with
+// 96 rows gated 653 us, 768, 1047.
 // y takes these blocks up to 192 rows per group, and up to 224 where there are at most
 // kFewTiles tiles, so that the start of a tile's copies under the tile before matters
 // less; past that those that stay (grouped_stream.h).  Their time by that of blocks that

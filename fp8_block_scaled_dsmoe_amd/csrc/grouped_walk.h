@@ -24,8 +24,8 @@ struct StreamSizes {
   uint32_t tiles_n;
 };
 
-// Tile `tile`, which is `step` behind the block's next one; false past the last.
-// Group g's rows are [begin[g], end[g]); y: first[g] row tiles come before them
+// A block's tile of number `tile`, which becomes that of its next one, `step` further;
+// false past the last.  Group g's rows are [begin[g], end[g]); y: first[g] row tiles come before them
 // (first[groups]: all), and walk is a group that tile's is not before.  read: of
 // a table's value.
 template <bool DW, int ROWS, int COLS, int CHUNK, typename Read>
